@@ -66,6 +66,19 @@ lib.fp8q_gemm_fused.restype = _st
 lib.fp8q_grouped_gemm_fused.argtypes = [_p, _i64, _p, _i32, _p, _p, _i64, _i64, _p, _i32, _i32,
                                         _p]
 lib.fp8q_grouped_gemm_fused.restype = _st
+lib.fp8q_quantize_token_i8.argtypes = [_p, _i64, _i64, _p, _p, _p]
+lib.fp8q_quantize_token_i8.restype = _st
+lib.fp8q_gemm_i8.argtypes = [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i32, _p]
+lib.fp8q_gemm_i8.restype = _st
+lib.fp8q_gemm_i8_gated.argtypes = [_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i32, _p]
+lib.fp8q_gemm_i8_gated.restype = _st
+lib.fp8q_gemm_gated.argtypes = [_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i32, _p, _p]
+lib.fp8q_gemm_gated.restype = _st
+lib.fp8q_grouped_gemm_gated.argtypes = [_p, _p, _i64, _p, _i32, _p, _p, _i64, _i64, _i32, _p, _i32,
+                                        _p, _p]
+lib.fp8q_grouped_gemm_gated.restype = _st
+lib.fp8q_gated_backward.argtypes = [_p, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _p, _p]
+lib.fp8q_gated_backward.restype = _st
 lib.fp8q_status_string.argtypes = [_st]
 lib.fp8q_status_string.restype = ctypes.c_char_p
 lib.fp8q_abi_version.argtypes = []
@@ -78,10 +91,13 @@ lib.fp8q_debug_checks.restype = ctypes.c_int
  ERR_OFFSETS) = range(9)
 SCALE_F32, SCALE_POW2 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1
 GROUP = 128
 
 _MODES = {"f32": SCALE_F32, "pow2": SCALE_POW2, SCALE_F32: SCALE_F32, SCALE_POW2: SCALE_POW2}
 _OUTS = {"f32": OUT_F32, "bf16": OUT_BF16, OUT_F32: OUT_F32, OUT_BF16: OUT_BF16}
+_ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, ACT_SILU: ACT_SILU,
+         ACT_GELU_TANH: ACT_GELU_TANH}
 
 
 class Fp8qError(RuntimeError):
@@ -147,7 +163,7 @@ def _ptr(t):
 def _dt(name):
     import torch
     return {"u8": torch.uint8, "f32": torch.float32, "bf16": torch.bfloat16,
-            "i32": torch.int32}[name]
+            "i32": torch.int32, "i8": torch.int8}[name]
 
 
 def _req(where, name, t, dtypes, shape, device):
@@ -387,6 +403,141 @@ def fp8q_gemm_rowscaled_precise(a_q, a_s, b_q, b_s, c, stream=None):
                                            _ptr(c), out, _stream(stream, a_q.device)), "fp8q_gemm_rowscaled_precise")
 
 
+def _act(where, act):
+    if act not in _ACTS:
+        raise ValueError(f"{where}: act = {act!r}, expected 'silu' or 'gelu_tanh'")
+    return _ACTS[act]
+
+
+def _mult16(where, **dims):
+    for k, v in dims.items():
+        if v % 16:
+            raise ValueError(f"{where}: {k} = {v} is not a multiple of 16")
+
+
+def fp8q_quantize_token_i8(x, q, s, stream=None):
+    """x: bf16 [M][K] -> q: int8 [M][Kp] (K up to a multiple of 16, zeros past
+    K), s: float32 [M], one scale per row (in place)."""
+    wh = "fp8q_quantize_token_i8"
+    M, K = _dims(wh, x, 2, "x")
+    _req(wh, "x", x, ["bf16"], (M, K), x.device)
+    _req(wh, "q", q, ["i8"], (M, -(-K // 16) * 16), x.device)
+    _req(wh, "s", s, ["f32"], (M,), x.device)
+    _invoke(lib.fp8q_quantize_token_i8, (_ptr(x), M, K, _ptr(q), _ptr(s),
+                                         _stream(stream, x.device)), wh)
+
+
+def fp8q_gemm_i8(a_q, a_s, w_q, w_s, c, bias=None, stream=None):
+    """c[M][N] (float32 or bfloat16) = (int8 a_q[M][K] x w_q[N][K]^T) * a_s[M]
+    * w_s[N] (+ bias[N])."""
+    wh = "fp8q_gemm_i8"
+    M, K = _dims(wh, a_q, 2, "a_q")
+    N, _ = _dims(wh, w_q, 2, "w_q")
+    _mult16(wh, K=K)
+    dev = a_q.device
+    _req(wh, "a_q", a_q, ["i8"], (M, K), dev)
+    _req(wh, "a_s", a_s, ["f32"], (M,), dev)
+    _req(wh, "w_q", w_q, ["i8"], (N, K), dev)
+    _req(wh, "w_s", w_s, ["f32"], (N,), dev)
+    _req(wh, "c", c, ["f32", "bf16"], (M, N), dev)
+    if bias is not None:
+        _req(wh, "bias", bias, ["f32"], (N,), dev)
+    _invoke(lib.fp8q_gemm_i8, (_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), _ptr(bias), M, N, K,
+                               _ptr(c), _out_code(wh, c), _stream(stream, dev)), wh)
+
+
+def fp8q_gemm_i8_gated(a_q, a_s, w_q, w_s, h, act="silu", stream=None):
+    """h[M][F] = act(Y[:, :F]) * Y[:, F:], Y the int8 product of a_q[M][K] with
+    the stacked gate and up weights w_q[2F][K], scaled by a_s[M] and w_s[2F]."""
+    wh = "fp8q_gemm_i8_gated"
+    M, K = _dims(wh, a_q, 2, "a_q")
+    N, _ = _dims(wh, w_q, 2, "w_q")
+    _mult16(wh, K=K)
+    if N % 2:
+        raise ValueError(f"{wh}: w_q has {N} rows, expected gate and up rows (an even number)")
+    dev = a_q.device
+    _req(wh, "a_q", a_q, ["i8"], (M, K), dev)
+    _req(wh, "a_s", a_s, ["f32"], (M,), dev)
+    _req(wh, "w_q", w_q, ["i8"], (N, K), dev)
+    _req(wh, "w_s", w_s, ["f32"], (N,), dev)
+    _req(wh, "h", h, ["f32", "bf16"], (M, N // 2), dev)
+    _invoke(lib.fp8q_gemm_i8_gated, (_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), M, N // 2, K,
+                                     _act(wh, act), _ptr(h), _out_code(wh, h),
+                                     _stream(stream, dev)), wh)
+
+
+def _gated_args(where, a_q, a_s, off, w_q, w_s, h, gate_up):
+    M, K = _dims(where, a_q, 2, "a_q")
+    if off is None:
+        N, _ = _dims(where, w_q, 2, "w_q")
+        lead = ()
+    else:
+        G, N, _ = _dims(where, w_q, 3, "w_q")
+        lead = (G,)
+    _mult128(where, K=K)
+    if N % (2 * GROUP):
+        raise ValueError(f"{where}: w_q has {N} rows, expected gate and up rows in multiples of "
+                         f"{GROUP} each")
+    dev = a_q.device
+    _req(where, "a_q", a_q, ["u8"], (M, K), dev)
+    _req(where, "a_s", a_s, ["f32"], (K // GROUP, M), dev)
+    if off is not None:
+        _req(where, "off", off, ["i32"], (lead[0] + 1,), dev)
+    _req(where, "w_q", w_q, ["u8"], lead + (N, K), dev)
+    _req(where, "w_s", w_s, ["f32"], lead + (N // GROUP, K // GROUP), dev)
+    _req(where, "h", h, ["f32", "bf16"], (M, N // 2), dev)
+    if gate_up is not None:
+        _req(where, "gate_up", gate_up, ["bf16"], (M, N), dev)
+    return M, N // 2, K, _out_code(where, h)
+
+
+def fp8q_gemm_gated(a_q, a_s, w_q, w_s, h, act="silu", gate_up=None, stream=None):
+    """h[M][F] = act(Y[:, :F]) * Y[:, F:], Y the block-scaled product of a_q
+    with the stacked gate and up weights w_q[2F][K]; gate_up (bf16 [M][2F], or
+    None) takes Y for the backward pass."""
+    wh = "fp8q_gemm_gated"
+    M, F, K, out = _gated_args(wh, a_q, a_s, None, w_q, w_s, h, gate_up)
+    _invoke(lib.fp8q_gemm_gated, (_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), M, F, K,
+                                  _act(wh, act), _ptr(h), out, _ptr(gate_up),
+                                  _stream(stream, a_q.device)), wh)
+
+
+def fp8q_grouped_gemm_gated(a_q, a_s, off, w_q, w_s, h, act="silu", gate_up=None, stream=None):
+    """fp8q_gemm_gated for routed experts: rows [off[e], off[e+1]) use expert
+    e's w_q[e][2F][K]; off is a device int32[G+1]."""
+    wh = "fp8q_grouped_gemm_gated"
+    _dims(wh, off, 1, "off")
+    M, F, K, out = _gated_args(wh, a_q, a_s, off, w_q, w_s, h, gate_up)
+    _invoke(lib.fp8q_grouped_gemm_gated, (_ptr(a_q), _ptr(a_s), M, _ptr(off), w_q.shape[0],
+                                          _ptr(w_q), _ptr(w_s), F, K, _act(wh, act), _ptr(h), out,
+                                          _ptr(gate_up), _stream(stream, a_q.device)), wh)
+
+
+def fp8q_gated_backward(dh, gate_up, q, s, qt, st, act="silu", mode="f32", stream=None):
+    """dY = [dh * up * act'(gate) | dh * act(gate)] of dh: bf16 [M][F] and
+    gate_up: bf16 [M][2F], quantized along the features (q: uint8 [M][2F], s:
+    float32 [2F/128][M]) and along the tokens (qt: uint8 [2F][Mp], st: float32
+    [Mp/128][2F], Mp = M up to a multiple of 128).  Either pair may be None."""
+    wh = "fp8q_gated_backward"
+    M, F = _dims(wh, dh, 2, "dh")
+    _mult128(wh, F=F)
+    dev = dh.device
+    _req(wh, "dh", dh, ["bf16"], (M, F), dev)
+    _req(wh, "gate_up", gate_up, ["bf16"], (M, 2 * F), dev)
+    if (q is None) != (s is None) or (qt is None) != (st is None) or (q is None and qt is None):
+        raise ValueError(f"{wh}: codes and scales come in pairs, and one pair at least")
+    if q is not None:
+        _req(wh, "q", q, ["u8"], (M, 2 * F), dev)
+        _req(wh, "s", s, ["f32"], (2 * F // GROUP, M), dev)
+    if qt is not None:
+        groups = -(-M // GROUP)
+        _req(wh, "qt", qt, ["u8"], (2 * F, groups * GROUP), dev)
+        _req(wh, "st", st, ["f32"], (groups, 2 * F), dev)
+    _invoke(lib.fp8q_gated_backward, (_ptr(dh), _ptr(gate_up), M, F, _act(wh, act), _MODES[mode],
+                                      _ptr(q), _ptr(s), _ptr(qt), _ptr(st),
+                                      _stream(stream, dev)), wh)
+
+
 # ---------------------------------------------------------- allocation helpers
 def quantize_act(x, mode="f32", stream=None):
     import torch
@@ -466,3 +617,71 @@ def grouped_gemm(a_q, a_s, off, w_q, w_s, out_dtype=None, stream=None, precise=F
     f = fp8q_grouped_gemm_precise if precise else fp8q_grouped_gemm
     f(a_q, a_s, off, w_q, w_s, c, stream)
     return c
+
+
+def quantize_token_i8(x, stream=None):
+    """x: bf16 [M][K] -> (int8 codes [M][Kp], float32 scales [M]); Kp is K up to
+    a multiple of 16, with zero codes past K."""
+    import torch
+    M, K = _dims("quantize_token_i8", x, 2, "x")
+    q = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=x.device)
+    s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    fp8q_quantize_token_i8(x, q, s, stream)
+    return q, s
+
+
+def gemm_i8(a_q, a_s, w_q, w_s, bias=None, out_dtype=None, stream=None):
+    import torch
+    c = torch.empty((a_q.shape[0], w_q.shape[0]), dtype=out_dtype or torch.float32,
+                    device=a_q.device)
+    fp8q_gemm_i8(a_q, a_s, w_q, w_s, c, bias, stream)
+    return c
+
+
+def gemm_i8_gated(a_q, a_s, w_q, w_s, act="silu", out_dtype=None, stream=None):
+    """h = act(gate) * up (bfloat16 unless out_dtype says float32)."""
+    import torch
+    h = torch.empty((a_q.shape[0], w_q.shape[0] // 2), dtype=out_dtype or torch.bfloat16,
+                    device=a_q.device)
+    fp8q_gemm_i8_gated(a_q, a_s, w_q, w_s, h, act, stream)
+    return h
+
+
+def gemm_gated(a_q, a_s, w_q, w_s, act="silu", out_dtype=None, save_gate_up=False, stream=None):
+    """h = act(gate) * up (bfloat16 unless out_dtype says float32); with
+    save_gate_up, (h, the bfloat16 [gate | up] the backward pass takes)."""
+    import torch
+    M, N = a_q.shape[0], w_q.shape[0]
+    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
+    gu = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device) if save_gate_up else None
+    fp8q_gemm_gated(a_q, a_s, w_q, w_s, h, act, gu, stream)
+    return (h, gu) if save_gate_up else h
+
+
+def grouped_gemm_gated(a_q, a_s, off, w_q, w_s, act="silu", out_dtype=None, save_gate_up=False,
+                       stream=None):
+    """gemm_gated by expert; rows at or past off[G] are not written."""
+    import torch
+    M, N = a_q.shape[0], w_q.shape[1]
+    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
+    gu = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device) if save_gate_up else None
+    fp8q_grouped_gemm_gated(a_q, a_s, off, w_q, w_s, h, act, gu, stream)
+    return (h, gu) if save_gate_up else h
+
+
+def gated_backward(dh, gate_up, act="silu", mode="f32", rows=True, tokens=True, stream=None):
+    """(q, s, qt, st): dY in E4M3 along the features and along the tokens, for
+    gemm (dX = dY W) and gemm_rowscaled (dW = dY^T X).  rows=False or
+    tokens=False leaves that pair out (None)."""
+    import torch
+    M, F = dh.shape
+    dev, groups = dh.device, -(-M // GROUP)
+    q = s = qt = st = None
+    if rows:
+        q = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
+        s = torch.empty((2 * F // GROUP, M), dtype=torch.float32, device=dev)
+    if tokens:
+        qt = torch.empty((2 * F, groups * GROUP), dtype=torch.uint8, device=dev)
+        st = torch.empty((groups, 2 * F), dtype=torch.float32, device=dev)
+    fp8q_gated_backward(dh, gate_up, q, s, qt, st, act, mode, stream)
+    return q, s, qt, st

@@ -1,0 +1,51 @@
+// Gate activations of the feed-forward block and their derivatives, in FP32.
+//
+// Both are x * sigma(y) with sigma the logistic function: SiLU has y = x, and
+// the tanh form of GELU, x/2 (1 + tanh z), is x * sigma(2z) because
+// 1 + tanh z = 2 sigma(2z).  In this form a large negative x keeps its
+// relative accuracy (1 + tanh z would cancel).  With s = sigma(y),
+//   d/dx x sigma(y) = s + x y' s (1 - s),  1 - s = exp(-y) s.
+// exp(-y) overflowing to infinity gives s = 0, so results stay finite for
+// every finite x.
+#pragma once
+
+#include "fp8q_device.hpp"
+
+namespace fp8q {
+
+constexpr int kActSilu = 0, kActGeluTanh = 1;
+// y = 2 sqrt(2/pi) (x + 0.044715 x^3) = kGelu1 x + kGelu3 x^3
+constexpr float kGelu1 = 1.5957691216057308f;
+constexpr float kGelu3 = 0.07135481282f;
+
+__device__ __forceinline__ float act_arg(int act, float x) {
+  return act == kActSilu ? x : x * (kGelu1 + kGelu3 * x * x);
+}
+
+// act(x), for a result that is rounded to BF16 or used in FP32 beside a
+// matrix product's own FP32 rounding: the hardware exponential and reciprocal
+// (each within 1 unit in the last place of FP32, the exponential's argument
+// scaled by log2 e) are far inside both.
+__device__ __forceinline__ float act_fast(int act, float x) {
+  const float e = __builtin_amdgcn_exp2f(act_arg(act, x) * -1.4426950408889634f);
+  return x * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// act(x) and act'(x) with the library exponential and correctly rounded
+// division: their results are quantized, and a code changes where an error
+// moves a value over a rounding boundary, so the error is kept at a few FP32
+// units.
+__device__ __forceinline__ void act_and_grad(int act, float x, float& a, float& da) {
+  const float e = expf(-act_arg(act, x));
+  const float s = 1.0f / (1.0f + e);
+  // 1 - s without cancellation where s is near 1; infinity * 0 is not a
+  // number, and fminf then gives the 1 that it stands for
+  const float r = fminf(e * s, 1.0f);
+  // beyond |x| = 1000 s (1 - s) is exactly 0; the clamp keeps x * y' finite there
+  const float xc = fminf(fmaxf(x, -1000.0f), 1000.0f);
+  const float dy = act == kActSilu ? 1.0f : kGelu1 + 3.0f * kGelu3 * xc * xc;
+  a = x * s;
+  da = s + xc * dy * (s * r);
+}
+
+}  // namespace fp8q

@@ -38,8 +38,23 @@ hipError_t launch_gemm_cast(const void* x, const uint8_t* w_q, const float* w_s,
 hipError_t launch_grouped_gemm_cast(const void* x, int64_t M_total, const int32_t* off, int G,
                                     const uint8_t* w_q, const float* w_s, int64_t N, int64_t K,
                                     void* c, int out_bf16, int mode, hipStream_t stream);
+hipError_t launch_quantize_token_i8(const void* x, int64_t M, int64_t K, int64_t Kp, int8_t* q,
+                                    float* s, hipStream_t stream);
+hipError_t launch_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
+                          const float* bias, int64_t M, int64_t N, int64_t K, void* c,
+                          int out_bf16, hipStream_t stream);
+hipError_t launch_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t* w_q,
+                                const float* w_s, int64_t M, int64_t F, int64_t K, int act,
+                                void* h, int out_bf16, hipStream_t stream);
+hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, const int32_t* off,
+                             int G, const uint8_t* w_q, const float* w_s, int64_t F, int64_t K,
+                             int act, void* h, int out_bf16, void* gu, hipStream_t stream);
+hipError_t launch_gated_backward(const void* dh, const void* gu, int64_t M, int64_t F, int act,
+                                 int mode, uint8_t* q, float* s, uint8_t* qt, float* st,
+                                 hipStream_t stream);
 #ifdef FP8Q_DEBUG_CHECKS
 hipError_t offsets_error_take(hipStream_t stream, int* flag);
+hipError_t gated_offsets_error_take(hipStream_t stream, int* flag);
 #endif
 }  // namespace fp8q
 
@@ -81,21 +96,24 @@ fp8q_status launched(hipError_t e) {
 
 // A grouped launch's status.  Debug builds (FP8Q_DEBUG_CHECKS) synchronize
 // the stream and report the kernel's verdict on the device offsets.
-fp8q_status grouped_launched(hipError_t e, hipStream_t stream) {
+fp8q_status grouped_launched(hipError_t e, hipStream_t stream, bool gated = false) {
   const fp8q_status st = launched(e);
 #ifdef FP8Q_DEBUG_CHECKS
   if (st == FP8Q_OK) {
     int flag = 0;
-    if (fp8q::offsets_error_take(stream, &flag) != hipSuccess) return launched(hipErrorUnknown);
+    auto take = gated ? fp8q::gated_offsets_error_take : fp8q::offsets_error_take;
+    if (take(stream, &flag) != hipSuccess) return launched(hipErrorUnknown);
     if (flag) return FP8Q_ERR_OFFSETS;
   }
 #else
   (void)stream;
+  (void)gated;
 #endif
   return st;
 }
 
 bool valid_mode(int m) { return m == FP8Q_SCALE_F32 || m == FP8Q_SCALE_POW2; }
+bool valid_act(int a) { return a == FP8Q_ACT_SILU || a == FP8Q_ACT_GELU_TANH; }
 bool valid_out(int o) { return o == FP8Q_OUT_F32 || o == FP8Q_OUT_BF16; }
 
 }  // namespace
@@ -367,6 +385,123 @@ fp8q_status fp8q_grouped_gemm_fused(const void* x_bf16, int64_t M_total, const i
                                                          K, c, out == FP8Q_OUT_BF16, (int)mode,
                                                          stream),
                           stream);
+}
+
+fp8q_status fp8q_quantize_token_i8(const void* x_bf16, int64_t M, int64_t K, int8_t* q, float* s,
+                                   hipStream_t stream) {
+  const bool empty = M == 0;
+  if (!empty && (!s || (K != 0 && (!x_bf16 || !q)))) return FP8Q_ERR_NULL;
+  if (M < 0 || K < 0) return FP8Q_ERR_SHAPE;
+  if (!aligned(x_bf16, 16) || !aligned(q, 16) || !aligned(s, 4)) return FP8Q_ERR_ALIGN;
+  if (empty) return FP8Q_OK;
+  if (K == 0) return FP8Q_ERR_UNSUPPORTED;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return launched(
+      fp8q::launch_quantize_token_i8(x_bf16, M, K, (K + 15) / 16 * 16, q, s, stream));
+}
+
+// Checks shared by the int8 products: `out_cols` output columns, `w_rows`
+// weight rows.  FP8Q_OK with *done set means there is nothing to compute.
+static fp8q_status i8_args(const int8_t* a_q, const float* a_s, const int8_t* w_q,
+                           const float* w_s, const float* bias, int64_t M, int64_t out_cols,
+                           int64_t K, const void* c, int out, bool* done) {
+  const bool empty_out = (M == 0 || out_cols == 0);
+  *done = true;
+  if (!empty_out && !c) return FP8Q_ERR_NULL;
+  if (!empty_out && K != 0 && (!a_q || !a_s || !w_q || !w_s)) return FP8Q_ERR_NULL;
+  if (M < 0 || out_cols < 0 || K < 0 || K % 16 != 0) return FP8Q_ERR_SHAPE;
+  if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(c, 16) || !aligned(a_s, 4) ||
+      !aligned(w_s, 4) || !aligned(bias, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_out(out)) return FP8Q_ERR_ENUM;
+  if (empty_out) return FP8Q_OK;
+  // 128 * 128 * K must stay below 2^31; K == 0 would need a fill kernel
+  if (K == 0 || K >= 131072) return FP8Q_ERR_UNSUPPORTED;
+  *done = false;
+  return FP8Q_OK;
+}
+
+fp8q_status fp8q_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
+                         const float* bias, int64_t M, int64_t N, int64_t K, void* c,
+                         fp8q_out_dtype out, hipStream_t stream) {
+  bool done;
+  fp8q_status st = i8_args(a_q, a_s, w_q, w_s, bias, M, N, K, c, out, &done);
+  if (st != FP8Q_OK || done) return st;
+  st = check_device();
+  if (st != FP8Q_OK) return st;
+  return launched(fp8q::launch_gemm_i8(a_q, a_s, w_q, w_s, bias, M, N, K, c,
+                                       out == FP8Q_OUT_BF16, stream));
+}
+
+fp8q_status fp8q_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t* w_q,
+                               const float* w_s, int64_t M, int64_t F, int64_t K,
+                               fp8q_activation act, void* h, fp8q_out_dtype out,
+                               hipStream_t stream) {
+  bool done;
+  fp8q_status st = i8_args(a_q, a_s, w_q, w_s, nullptr, M, F, K, h, out, &done);
+  if (st == FP8Q_OK && !valid_act(act)) st = FP8Q_ERR_ENUM;
+  if (st != FP8Q_OK || done) return st;
+  st = check_device();
+  if (st != FP8Q_OK) return st;
+  return launched(fp8q::launch_gemm_i8_gated(a_q, a_s, w_q, w_s, M, F, K, act, h,
+                                             out == FP8Q_OUT_BF16, stream));
+}
+
+// off NULL and G 0: the dense call.
+static fp8q_status gated_call(const uint8_t* a_q, const float* a_s, int64_t M, bool grouped,
+                              const int32_t* off, int32_t G, const uint8_t* w_q, const float* w_s,
+                              int64_t F, int64_t K, int act, void* h, int out, void* gate_up,
+                              hipStream_t stream) {
+  const bool empty_out = (M == 0 || F == 0);
+  if (grouped && !off) return FP8Q_ERR_NULL;
+  if (!empty_out && !h) return FP8Q_ERR_NULL;
+  if (!empty_out && K != 0 && (!a_q || !a_s || !w_q || !w_s)) return FP8Q_ERR_NULL;
+  if (M < 0 || F < 0 || K < 0 || F % 128 != 0 || K % 128 != 0) return FP8Q_ERR_SHAPE;
+  if (grouped && (G < 1 || M > 0x7FFFFFFF)) return FP8Q_ERR_SHAPE;  // offsets are int32
+  if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(h, 16) || !aligned(gate_up, 16) ||
+      !aligned(a_s, 4) || !aligned(w_s, 4) || !aligned(off, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_act(act) || !valid_out(out)) return FP8Q_ERR_ENUM;
+  if (grouped && G > 1024) return FP8Q_ERR_UNSUPPORTED;
+  if (empty_out) return FP8Q_OK;
+  if (K == 0 || !gemm_extent_ok(M, K)) return FP8Q_ERR_UNSUPPORTED;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  const hipError_t e = fp8q::launch_gemm_gated(a_q, a_s, M, off, G, w_q, w_s, F, K, act, h,
+                                               out == FP8Q_OUT_BF16, gate_up, stream);
+  return grouped ? grouped_launched(e, stream, true) : launched(e);
+}
+
+fp8q_status fp8q_gemm_gated(const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
+                            const float* w_s, int64_t M, int64_t F, int64_t K,
+                            fp8q_activation act, void* h, fp8q_out_dtype out, void* gate_up,
+                            hipStream_t stream) {
+  return gated_call(a_q, a_s, M, false, nullptr, 0, w_q, w_s, F, K, act, h, out, gate_up, stream);
+}
+
+fp8q_status fp8q_grouped_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M_total,
+                                    const int32_t* off, int32_t G, const uint8_t* w_q,
+                                    const float* w_s, int64_t F, int64_t K, fp8q_activation act,
+                                    void* h, fp8q_out_dtype out, void* gate_up,
+                                    hipStream_t stream) {
+  return gated_call(a_q, a_s, M_total, true, off, G, w_q, w_s, F, K, act, h, out, gate_up, stream);
+}
+
+fp8q_status fp8q_gated_backward(const void* dh, const void* gate_up, int64_t M, int64_t F,
+                                fp8q_activation act, fp8q_scale_mode mode, uint8_t* q, float* s,
+                                uint8_t* qt, float* st, hipStream_t stream) {
+  const bool empty = (M == 0 || F == 0);
+  if (!empty && (!dh || !gate_up || !q != !s || !qt != !st || (!q && !qt))) return FP8Q_ERR_NULL;
+  if (M < 0 || F < 0 || F % 128 != 0) return FP8Q_ERR_SHAPE;
+  if (!aligned(dh, 16) || !aligned(gate_up, 16) || !aligned(q, 16) || !aligned(qt, 16) ||
+      !aligned(s, 4) || !aligned(st, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_act(act) || !valid_mode(mode)) return FP8Q_ERR_ENUM;
+  if (empty) return FP8Q_OK;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return launched(fp8q::launch_gated_backward(dh, gate_up, M, F, act, mode, q, s, qt, st, stream));
 }
 
 }  // extern "C"

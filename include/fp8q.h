@@ -338,6 +338,122 @@ fp8q_status fp8q_grouped_gemm_fused(const void* x_bf16, int64_t M_total,
                                     void* c, fp8q_out_dtype out, fp8q_scale_mode mode,
                                     hipStream_t stream);
 
+/*
+ * The feed-forward layer in 8 bits (the calls below): products of int8 codes
+ * with one scale per token and per output channel, the gated block
+ * act(gate) * up on int8 and on block-scaled E4M3 operands, and the backward
+ * pass of its activation.
+ */
+typedef enum {
+  FP8Q_ACT_SILU = 0,      /* act(x) = x / (1 + exp(-x))                                  */
+  FP8Q_ACT_GELU_TANH = 1  /* act(x) = x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))      */
+} fp8q_activation;
+
+/*
+ * Per-token symmetric int8 quantization (per output channel for a weight
+ * matrix [N][K]):
+ *   s[m] = fl32(amax_m / 127),
+ *   q[m][k] = rne(fl32(x[m][k] * inv_m)), inv_m = fl32(127 * fl32(1 / amax_m)).
+ * A row whose inv is not finite (amax 0 or below 127/FLT_MAX) is flushed: s = 0
+ * and every code 0.
+ *   x_bf16 : [M][K] bfloat16, row-major; 16-byte aligned.
+ *   q      : [M][Kp] int8 codes in [-127, 127] (output), Kp = K rounded up to a
+ *            multiple of 16, zeros past K; 16-byte aligned.
+ *   s      : [M] float32 (output); 4-byte aligned.
+ *   M >= 0 (M == 0 is a no-op), any K >= 1 (K == 0 with M > 0: FP8Q_ERR_UNSUPPORTED).
+ * Results are bit-exact functions of the input.
+ */
+fp8q_status fp8q_quantize_token_i8(const void* x_bf16, int64_t M, int64_t K, int8_t* q, float* s,
+                                   hipStream_t stream);
+
+/*
+ * int8 product with scales per token and per channel:
+ *   C[m][n] = (sum_k a_q[m][k] * w_q[n][k]) * a_s[m] * w_s[n] + bias[n].
+ *   a_q : [M][K] int8, a_s : [M] float32; w_q : [N][K] int8, w_s : [N] float32
+ *         (as from fp8q_quantize_token_i8; the code -128 is allowed too)
+ *   bias: [N] float32, or NULL for none; 4-byte aligned.
+ *   c   : [M][N] float32 or bfloat16 (per `out`), row-major (output).
+ *   M >= 0, any N >= 0, K % 16 == 0.
+ * FP8Q_ERR_UNSUPPORTED: K == 0 with M*N > 0, or K >= 131072 (the sum could
+ *   leave int32).
+ * Accuracy: the integer sum is exact; it is converted to FP32 and scaled by
+ * two FP32 products (and one addition), so
+ *   |C - C_exact| <= 4 * 2^-24 * (|C_exact - bias| + |bias|)  (+ half a BF16 ulp).
+ */
+fp8q_status fp8q_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
+                         const float* bias, int64_t M, int64_t N, int64_t K, void* c,
+                         fp8q_out_dtype out, hipStream_t stream);
+
+/*
+ * Gated block on int8 operands: with Y = fp8q_gemm_i8's product (no bias) of
+ * the stacked gate and up weights,
+ *   h[m][f] = act(Y[m][f]) * Y[m][F + f],
+ * formed in FP32 from the exact integer sums; Y is not written.
+ *   a_q : [M][K] int8, a_s : [M] float32;
+ *   w_q : [2F][K] int8 (rows 0..F-1 gate, F..2F-1 up), w_s : [2F] float32
+ *   h   : [M][F] float32 or bfloat16 (per `out`) (output).
+ *   M >= 0, any F >= 0, K % 16 == 0; errors as fp8q_gemm_i8.
+ */
+fp8q_status fp8q_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t* w_q,
+                               const float* w_s, int64_t M, int64_t F, int64_t K,
+                               fp8q_activation act, void* h, fp8q_out_dtype out,
+                               hipStream_t stream);
+
+/*
+ * Gated block on block-scaled E4M3 operands: with Y = fp8q_gemm's product of
+ * the stacked gate and up weights (accuracy clause of fp8q_gemm),
+ *   h[m][f] = act(Y[m][f]) * Y[m][F + f].
+ *   a_q : [M][K] uint8, a_s : [K/128][M] float32 (from fp8q_quantize_act)
+ *   w_q : [2F][K] uint8 (rows 0..F-1 gate, F..2F-1 up), w_s : [2F/128][K/128]
+ *         float32 (from fp8q_quantize_weight)
+ *   h   : [M][F] float32 or bfloat16 (per `out`) (output).
+ *   gate_up : [M][2F] bfloat16 Y for the backward pass (output), or NULL;
+ *         h is formed from the FP32 Y, not from this rounded copy.
+ *   M >= 0, F % 128 == 0, K % 128 == 0; errors as fp8q_gemm.
+ * act is evaluated in FP32 with a relative error below 2^-20 in act(x).
+ */
+fp8q_status fp8q_gemm_gated(const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
+                            const float* w_s, int64_t M, int64_t F, int64_t K,
+                            fp8q_activation act, void* h, fp8q_out_dtype out, void* gate_up,
+                            hipStream_t stream);
+
+/*
+ * The same for routed experts: rows [off[e], off[e+1]) use expert e's weights.
+ *   off : DEVICE int32[G+1], as for fp8q_grouped_gemm (validated on the device:
+ *         with invalid offsets nothing is written).
+ *   w_q : [G][2F][K] uint8, w_s : [G][2F/128][K/128] float32.
+ *   h   : [M_total][F], gate_up : [M_total][2F] or NULL; rows >= off[G] are
+ *         left untouched.
+ *   Errors as fp8q_grouped_gemm.
+ */
+fp8q_status fp8q_grouped_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M_total,
+                                    const int32_t* off, int32_t G, const uint8_t* w_q,
+                                    const float* w_s, int64_t F, int64_t K, fp8q_activation act,
+                                    void* h, fp8q_out_dtype out, void* gate_up,
+                                    hipStream_t stream);
+
+/*
+ * Backward pass of the gated activation, quantized for both gradient GEMMs of
+ * the gate/up projection in one pass over its inputs:
+ *   dgate = dh * up * act'(gate), dup = dh * act(gate), dY = [dgate | dup] in
+ *   FP32, then (scale rule `mode`, as fp8q_quantize_act)
+ *   q, s   : dY in 1x128 groups along the features: [M][2F] codes and
+ *            [2F/128][M] scales (the A operand of dX = dY W);
+ *   qt, st : dY^T in groups of 128 tokens: [2F][Mp] codes and [Mp/128][2F]
+ *            scales, Mp = M rounded up to a multiple of 128, codes past M zero
+ *            (the A operand of dW = dY^T X, fp8q_gemm_rowscaled).
+ * Either pair may be NULL: it is then not computed.
+ *   dh      : [M][F] bfloat16; gate_up : [M][2F] bfloat16 (from fp8q_gemm_gated).
+ *   M >= 0, F >= 0 with F % 128 == 0.
+ * dY is not rounded before it is quantized; its FP32 values carry a relative
+ * error of a few 2^-24, so a code can differ from that of the exact dY only
+ * where the exact value lies that close to a rounding boundary.
+ * RANGE: dY must stay below FLT_MAX.
+ */
+fp8q_status fp8q_gated_backward(const void* dh, const void* gate_up, int64_t M, int64_t F,
+                                fp8q_activation act, fp8q_scale_mode mode, uint8_t* q, float* s,
+                                uint8_t* qt, float* st, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* fp8q_status_string(fp8q_status status);
 

@@ -39,6 +39,8 @@ Modules:
               evaluated by a plain C loop (truncation_bound.c) for full-size
               matrices
   native      builds and loads that C loop (libtbound.so)
+  feed_forward int8 per-token quantizer and product, gated activation and its
+              backward pass, in float64
   narrow_acc  emulator of a narrow fixed-point accumulator (accuracy study)
 """
 
