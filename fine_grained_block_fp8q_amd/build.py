@@ -46,6 +46,7 @@ SOURCES = {
                          "-mllvm", "-pragma-unroll-threshold=60000"],
     "token_quant.hip": ["-ffp-contract=off"],
     "few_rows.hip": [],
+    "i8_tiles.hip": [],
     "gated_backward.hip": [],
     "fp8q_api.hip": [],
 }

@@ -294,9 +294,9 @@ static hipError_t launch_few(FewArgs p, int64_t row_blocks_extra, hipStream_t st
   return hipGetLastError();
 }
 
-hipError_t launch_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
-                          const float* bias, int64_t M, int64_t N, int64_t K, void* c,
-                          int out_bf16, hipStream_t stream) {
+hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
+                         const float* bias, int64_t M, int64_t N, int64_t K, bool gated, int act,
+                         void* c, int out_bf16, hipStream_t stream) {
   FewArgs p{};
   p.a = reinterpret_cast<const uint8_t*>(a_q);
   p.a_s = a_s;
@@ -307,25 +307,10 @@ hipError_t launch_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q
   p.M = M;
   p.N = N;
   p.K = K;
-  p.out_bf16 = out_bf16;
-  return launch_few<kFewI8, false, false>(p, 0, stream);
-}
-
-hipError_t launch_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t* w_q,
-                                const float* w_s, int64_t M, int64_t F, int64_t K, int act,
-                                void* h, int out_bf16, hipStream_t stream) {
-  FewArgs p{};
-  p.a = reinterpret_cast<const uint8_t*>(a_q);
-  p.a_s = a_s;
-  p.w = reinterpret_cast<const uint8_t*>(w_q);
-  p.w_s = w_s;
-  p.c = h;
-  p.M = M;
-  p.N = F;
-  p.K = K;
   p.act = act;
   p.out_bf16 = out_bf16;
-  return launch_few<kFewI8, true, false>(p, 0, stream);
+  return gated ? launch_few<kFewI8, true, false>(p, 0, stream)
+               : launch_few<kFewI8, false, false>(p, 0, stream);
 }
 
 // off NULL: one dense block of weights; else G experts.
