@@ -48,4 +48,12 @@ __device__ __forceinline__ void act_and_grad(int act, float x, float& a, float& 
   da = s + xc * dy * (s * r);
 }
 
+// Two floats -> two bfloat16, round to nearest even (one instruction), a in the
+// low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
+}
+
 }  // namespace fp8q

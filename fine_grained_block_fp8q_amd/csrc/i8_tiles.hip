@@ -54,7 +54,10 @@ struct I8Cfg {
   static_assert(WM % 16 == 0 && WN % (GATED ? 32 : 16) == 0, "whole blocks");
   static_assert(NA * LA + NW * LW < 64, "loads in flight");
   static_assert(LDS <= 160 * 1024, "LDS budget");
-  static_assert(LDS / NWAVES >= 16 * (WNO * 4 + 16) + WN * 8, "an output block fits the wave's share");
+  // row blocks of outputs that a wave's share of the ring holds
+  static constexpr int ROW_BLOCKS = BF16 || WNO < 128 ? MB : MB / 2;
+  static_assert(LDS / NWAVES >= ROW_BLOCKS * 16 * (WNO * (BF16 ? 2 : 4) + 16) + WN * 8,
+                "they fit it, with the columns' scales");
 };
 
 struct I8Args {
@@ -109,25 +112,7 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
   const int64_t m0 = (int64_t)tm * Cfg::BM, n0 = (int64_t)tn * Cfg::OBN;
   const int64_t K = p.K;
 
-  // The rows' and columns' scales and the bias, for the epilogue.  They are
-  // asked for before the ring's loads, so that waiting for them does not wait
-  // for those.
   const int fr = lane & 15, fq = lane >> 4;
-  constexpr int CS = (Cfg::WN + 63) / 64;
-  float scale[CS], bias[CS], row_scale[MB];
-#pragma unroll
-  for (int x = 0; x < CS; ++x) {
-    const int o = (lane + 64 * x) % Cfg::WN;
-    const int64_t n = n0 + wave_n * Cfg::WNO + o % Cfg::WNO;
-    const int64_t nn = n < p.N ? n : p.N - 1;
-    scale[x] = p.w_s[nn + (o >= Cfg::WNO ? p.N : 0)];
-    bias[x] = !Cfg::GATED && p.bias ? p.bias[nn] : 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int64_t m = m0 + wave_m * Cfg::WM + 16 * i + fr;
-    row_scale[i] = p.a_s[m < p.M ? m : p.M - 1];
-  }
 
   // ---- loads.  Load d of a wave is rows 8(d NWAVES + wave) .. +7 of the unit:
   // lane l fetches row l/8, physical piece l%8 of it.  The row block and the
@@ -271,6 +256,23 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
     step1(g + 1, a1[1], a1[0], u1, u2);
     u = u2;
   }
+  // The rows' and columns' scales and the bias, for the epilogue.  (Asked for
+  // before the loop they would be spilled there, each with a wait of its own.)
+  constexpr int CS = (Cfg::WN + 63) / 64;
+  float scale[CS], bias[CS], row_scale[MB];
+#pragma unroll
+  for (int x = 0; x < CS; ++x) {
+    const int o = (lane + 64 * x) % Cfg::WN;
+    const int64_t n = n0 + wave_n * Cfg::WNO + o % Cfg::WNO;
+    const int64_t nn = n < p.N ? n : p.N - 1;
+    scale[x] = p.w_s[nn + (o >= Cfg::WNO ? p.N : 0)];
+    bias[x] = !Cfg::GATED && p.bias ? p.bias[nn] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    const int64_t m = m0 + wave_m * Cfg::WM + 16 * i + fr;
+    row_scale[i] = p.a_s[m < p.M ? m : p.M - 1];
+  }
   // the last products' results, before the vector ALU reads them
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
   wait_vmcnt<0>();
@@ -292,44 +294,53 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
   const int64_t nw = n0 + wave_n * Cfg::WNO;  // the wave's first output column
   const int live_n = (int)(p.N - nw < Cfg::WNO ? (p.N - nw > 0 ? p.N - nw : 0) : Cfg::WNO);
   const bool vec = (p.N * OB) % 16 == 0;  // every row of C starts at a 16-byte boundary
+  // As many row blocks at a time as the wave's share holds, then one loop that
+  // stores them: the code runs once a tile, and what it costs is to fetch it.
+  constexpr int NO = Cfg::WNO / 16, IB = Cfg::ROW_BLOCKS;
+  v4f s_w[NO], more[NO];  // more: the up rows' scales when gated, else the bias
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int64_t mb = m0 + wave_m * Cfg::WM + 16 * i;
+  for (int j = 0; j < NO; ++j) {
+    s_w[j] = *reinterpret_cast<const v4f*>(ws + 16 * j + 4 * fq);
+    more[j] =
+        *reinterpret_cast<const v4f*>(ws + (Cfg::GATED ? Cfg::WNO : Cfg::WN) + 16 * j + 4 * fq);
+  }
 #pragma unroll
-    for (int j = 0; j < Cfg::WNO / 16; ++j) {
-      const int o = 16 * j + 4 * fq;
-      const v4f s_w = *reinterpret_cast<const v4f*>(ws + o);
-      // gated: the up rows' scales; else the bias
-      const v4f more = *reinterpret_cast<const v4f*>(ws + (Cfg::GATED ? Cfg::WNO : Cfg::WN) + o);
-      float v[4];
+  for (int i0 = 0; i0 < MB; i0 += IB) {
+    const int64_t mb = m0 + wave_m * Cfg::WM + 16 * i0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = (float)acc[i][j][e] * row_scale[i] * s_w[e];
-        if constexpr (Cfg::GATED)
-          v[e] = act_fast(p.act, v[e]) * ((float)acc[i][j + NB / 2][e] * row_scale[i] * more[e]);
+    for (int i = i0; i < i0 + IB; ++i)
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = (float)acc[i][j][e] * row_scale[i];
+          if constexpr (Cfg::GATED)
+            v[e] = act_fast(p.act, v[e] * s_w[j][e]) *
+                   ((float)acc[i][j + NB / 2][e] * row_scale[i] * more[j][e]);
+          else
+            v[e] = __builtin_fmaf(v[e], s_w[j][e], more[j][e]);
+        }
+        uint8_t* at = rows + (16 * (i - i0) + fr) * PITCH + (16 * j + 4 * fq) * OB;
+        if constexpr (Cfg::BF16)
+          *reinterpret_cast<v2u*>(at) = v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         else
-          v[e] += more[e];
+          *reinterpret_cast<v4f*>(at) = v4f{v[0], v[1], v[2], v[3]};
       }
-      if constexpr (Cfg::BF16)
-        *reinterpret_cast<v2u*>(rows + fr * PITCH + o * 2) =
-            v2u{f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
-                f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16};
-      else
-        *reinterpret_cast<v4f*>(rows + fr * PITCH + o * 4) = v4f{v[0], v[1], v[2], v[3]};
-    }
     lds_wave_fence();
+    const int live_m = (int)(p.M - mb < 16 * IB ? (p.M - mb > 0 ? p.M - mb : 0) : 16 * IB);
     if (vec) {
-#pragma unroll
-      for (int x0 = 0; x0 < 16 * PER; x0 += 64) {
-        const int r = (x0 + lane) / PER, c = (x0 + lane) % PER;
-        if (r < 16 && mb + r < p.M && c * 16 < live_n * OB)
+#pragma unroll 4
+      for (int x = lane; x < 16 * IB * PER; x += 64) {
+        const int r = x / PER, c = x % PER;
+        if (r < live_m && c * 16 < live_n * OB)
           *reinterpret_cast<v4u*>(static_cast<uint8_t*>(p.c) + ((mb + r) * p.N + nw) * OB + c * 16) =
               *reinterpret_cast<const v4u*>(rows + r * PITCH + c * 16);
       }
     } else {
-      for (int x = lane; x < 16 * Cfg::WNO; x += 64) {
+      for (int x = lane; x < 16 * IB * Cfg::WNO; x += 64) {
         const int r = x / Cfg::WNO, c = x % Cfg::WNO;
-        if (mb + r < p.M && c < live_n) {
+        if (r < live_m && c < live_n) {
           const int64_t at = (mb + r) * p.N + nw + c;
           if constexpr (Cfg::BF16)
             static_cast<uint16_t*>(p.c)[at] = *reinterpret_cast<const uint16_t*>(rows + r * PITCH + c * 2);
