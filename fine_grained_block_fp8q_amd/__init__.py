@@ -160,10 +160,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_DTYPES = {"u8": "uint8", "f32": "float32", "bf16": "bfloat16", "i32": "int32", "i8": "int8"}
+
+
 def _dt(name):
     import torch
-    return {"u8": torch.uint8, "f32": torch.float32, "bf16": torch.bfloat16,
-            "i32": torch.int32, "i8": torch.int8}[name]
+    return getattr(torch, _DTYPES[name])
 
 
 def _req(where, name, t, dtypes, shape, device):
@@ -207,6 +209,8 @@ def _out_code(where, c):
 def _stream(stream, device):
     import torch
     if stream is None:
+        if device.type == "cuda":     # the handle alone, without a Stream object around it
+            return torch._C._cuda_getCurrentRawStream(device.index)
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -403,92 +407,120 @@ def fp8q_gemm_rowscaled_precise(a_q, a_s, b_q, b_s, c, stream=None):
                                            _ptr(c), out, _stream(stream, a_q.device)), "fp8q_gemm_rowscaled_precise")
 
 
+def _need(where, dev, *tensors):
+    """_req of several (name, tensor, dtype, shape) on one device.  Nothing is
+    looked up while all is right: calls that serve single tokens take about as
+    long as their checks."""
+    for name, t, dt, shape in tensors:
+        try:
+            if t.dtype is dt and t.shape == shape and t.device == dev and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _req(where, name, t, [next(k for k in _DTYPES if _dt(k) is dt)], shape, dev)
+
+
 def _act(where, act):
     if act not in _ACTS:
         raise ValueError(f"{where}: act = {act!r}, expected 'silu' or 'gelu_tanh'")
     return _ACTS[act]
 
 
-def _mult16(where, **dims):
-    for k, v in dims.items():
-        if v % 16:
-            raise ValueError(f"{where}: {k} = {v} is not a multiple of 16")
-
-
 def fp8q_quantize_token_i8(x, q, s, stream=None):
     """x: bf16 [M][K] -> q: int8 [M][Kp] (K up to a multiple of 16, zeros past
     K), s: float32 [M], one scale per row (in place)."""
+    import torch
     wh = "fp8q_quantize_token_i8"
     M, K = _dims(wh, x, 2, "x")
-    _req(wh, "x", x, ["bf16"], (M, K), x.device)
-    _req(wh, "q", q, ["i8"], (M, -(-K // 16) * 16), x.device)
-    _req(wh, "s", s, ["f32"], (M,), x.device)
-    _invoke(lib.fp8q_quantize_token_i8, (_ptr(x), M, K, _ptr(q), _ptr(s),
-                                         _stream(stream, x.device)), wh)
+    _need(wh, x.device, ("q", q, torch.int8, (M, -(-K // 16) * 16)), ("s", s, torch.float32, (M,)))
+    _quantize_token_i8(wh, x, M, K, q, s, stream)
+
+
+def _quantize_token_i8(wh, x, M, K, q, s, stream):
+    import torch
+    dev = x.device
+    _need(wh, dev, ("x", x, torch.bfloat16, (M, K)))
+    _invoke(lib.fp8q_quantize_token_i8, (x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(),
+                                         _stream(stream, dev)), wh)
+
+
+def _rows(where, a_q, w_q):
+    """Rows of both operands, for the output's shape."""
+    return _dims(where, a_q, 2, "a_q")[0], _dims(where, w_q, 2, "w_q")[0]
+
+
+def _i8_args(where, a_q, a_s, w_q, w_s):
+    import torch
+    M, K = _dims(where, a_q, 2, "a_q")
+    N, _ = _dims(where, w_q, 2, "w_q")
+    if K % 16:
+        raise ValueError(f"{where}: K = {K} is not a multiple of 16")
+    dev = a_q.device
+    _need(where, dev, ("a_q", a_q, torch.int8, (M, K)), ("a_s", a_s, torch.float32, (M,)),
+          ("w_q", w_q, torch.int8, (N, K)), ("w_s", w_s, torch.float32, (N,)))
+    return M, N, K, dev
 
 
 def fp8q_gemm_i8(a_q, a_s, w_q, w_s, c, bias=None, stream=None):
     """c[M][N] (float32 or bfloat16) = (int8 a_q[M][K] x w_q[N][K]^T) * a_s[M]
     * w_s[N] (+ bias[N])."""
     wh = "fp8q_gemm_i8"
-    M, K = _dims(wh, a_q, 2, "a_q")
-    N, _ = _dims(wh, w_q, 2, "w_q")
-    _mult16(wh, K=K)
-    dev = a_q.device
-    _req(wh, "a_q", a_q, ["i8"], (M, K), dev)
-    _req(wh, "a_s", a_s, ["f32"], (M,), dev)
-    _req(wh, "w_q", w_q, ["i8"], (N, K), dev)
-    _req(wh, "w_s", w_s, ["f32"], (N,), dev)
-    _req(wh, "c", c, ["f32", "bf16"], (M, N), dev)
+    M, N = _rows(wh, a_q, w_q)
+    _req(wh, "c", c, ["f32", "bf16"], (M, N), a_q.device)
+    _gemm_i8(wh, a_q, a_s, w_q, w_s, c, bias, stream)
+
+
+def _gemm_i8(wh, a_q, a_s, w_q, w_s, c, bias, stream):
+    M, N, K, dev = _i8_args(wh, a_q, a_s, w_q, w_s)
     if bias is not None:
         _req(wh, "bias", bias, ["f32"], (N,), dev)
-    _invoke(lib.fp8q_gemm_i8, (_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), _ptr(bias), M, N, K,
-                               _ptr(c), _out_code(wh, c), _stream(stream, dev)), wh)
+    _invoke(lib.fp8q_gemm_i8, (a_q.data_ptr(), a_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(),
+                               bias.data_ptr() if bias is not None else None, M, N, K,
+                               c.data_ptr(), _out_code(wh, c), _stream(stream, dev)), wh)
+
+
+def _gate_rows(where, N, multiple):
+    if N % (2 * multiple):
+        raise ValueError(f"{where}: w_q has {N} rows, expected gate and up rows"
+                         + (f" in multiples of {multiple} each" if multiple > 1 else ""))
 
 
 def fp8q_gemm_i8_gated(a_q, a_s, w_q, w_s, h, act="silu", stream=None):
     """h[M][F] = act(Y[:, :F]) * Y[:, F:], Y the int8 product of a_q[M][K] with
     the stacked gate and up weights w_q[2F][K], scaled by a_s[M] and w_s[2F]."""
     wh = "fp8q_gemm_i8_gated"
-    M, K = _dims(wh, a_q, 2, "a_q")
-    N, _ = _dims(wh, w_q, 2, "w_q")
-    _mult16(wh, K=K)
-    if N % 2:
-        raise ValueError(f"{wh}: w_q has {N} rows, expected gate and up rows (an even number)")
-    dev = a_q.device
-    _req(wh, "a_q", a_q, ["i8"], (M, K), dev)
-    _req(wh, "a_s", a_s, ["f32"], (M,), dev)
-    _req(wh, "w_q", w_q, ["i8"], (N, K), dev)
-    _req(wh, "w_s", w_s, ["f32"], (N,), dev)
-    _req(wh, "h", h, ["f32", "bf16"], (M, N // 2), dev)
-    _invoke(lib.fp8q_gemm_i8_gated, (_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), M, N // 2, K,
-                                     _act(wh, act), _ptr(h), _out_code(wh, h),
-                                     _stream(stream, dev)), wh)
+    M, N = _rows(wh, a_q, w_q)
+    _req(wh, "h", h, ["f32", "bf16"], (M, N // 2), a_q.device)
+    _gemm_i8_gated(wh, a_q, a_s, w_q, w_s, h, act, stream)
+
+
+def _gemm_i8_gated(wh, a_q, a_s, w_q, w_s, h, act, stream):
+    M, N, K, dev = _i8_args(wh, a_q, a_s, w_q, w_s)
+    _gate_rows(wh, N, 1)
+    _invoke(lib.fp8q_gemm_i8_gated, (a_q.data_ptr(), a_s.data_ptr(), w_q.data_ptr(),
+                                     w_s.data_ptr(), M, N // 2, K, _act(wh, act), h.data_ptr(),
+                                     _out_code(wh, h), _stream(stream, dev)), wh)
 
 
 def _gated_args(where, a_q, a_s, off, w_q, w_s, h, gate_up):
+    import torch
     M, K = _dims(where, a_q, 2, "a_q")
-    if off is None:
-        N, _ = _dims(where, w_q, 2, "w_q")
-        lead = ()
-    else:
-        G, N, _ = _dims(where, w_q, 3, "w_q")
-        lead = (G,)
-    _mult128(where, K=K)
-    if N % (2 * GROUP):
-        raise ValueError(f"{where}: w_q has {N} rows, expected gate and up rows in multiples of "
-                         f"{GROUP} each")
-    dev = a_q.device
-    _req(where, "a_q", a_q, ["u8"], (M, K), dev)
-    _req(where, "a_s", a_s, ["f32"], (K // GROUP, M), dev)
+    lead = ()
     if off is not None:
-        _req(where, "off", off, ["i32"], (lead[0] + 1,), dev)
-    _req(where, "w_q", w_q, ["u8"], lead + (N, K), dev)
-    _req(where, "w_s", w_s, ["f32"], lead + (N // GROUP, K // GROUP), dev)
+        lead = (_dims(where, w_q, 3, "w_q")[0],)
+    N = _dims(where, w_q, 2 + len(lead), "w_q")[-2]
+    _mult128(where, K=K)
+    _gate_rows(where, N, GROUP)
+    dev = a_q.device
+    _need(where, dev, ("a_q", a_q, torch.uint8, (M, K)),
+          ("a_s", a_s, torch.float32, (K // GROUP, M)), ("w_q", w_q, torch.uint8, lead + (N, K)),
+          ("w_s", w_s, torch.float32, lead + (N // GROUP, K // GROUP)))
+    if off is not None:
+        _need(where, dev, ("off", off, torch.int32, (lead[0] + 1,)))
     _req(where, "h", h, ["f32", "bf16"], (M, N // 2), dev)
     if gate_up is not None:
-        _req(where, "gate_up", gate_up, ["bf16"], (M, N), dev)
-    return M, N // 2, K, _out_code(where, h)
+        _need(where, dev, ("gate_up", gate_up, torch.bfloat16, (M, N)))
+    return M, N // 2, K, _out_code(where, h), dev
 
 
 def fp8q_gemm_gated(a_q, a_s, w_q, w_s, h, act="silu", gate_up=None, stream=None):
@@ -496,10 +528,11 @@ def fp8q_gemm_gated(a_q, a_s, w_q, w_s, h, act="silu", gate_up=None, stream=None
     with the stacked gate and up weights w_q[2F][K]; gate_up (bf16 [M][2F], or
     None) takes Y for the backward pass."""
     wh = "fp8q_gemm_gated"
-    M, F, K, out = _gated_args(wh, a_q, a_s, None, w_q, w_s, h, gate_up)
-    _invoke(lib.fp8q_gemm_gated, (_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), M, F, K,
-                                  _act(wh, act), _ptr(h), out, _ptr(gate_up),
-                                  _stream(stream, a_q.device)), wh)
+    M, F, K, out, dev = _gated_args(wh, a_q, a_s, None, w_q, w_s, h, gate_up)
+    _invoke(lib.fp8q_gemm_gated, (a_q.data_ptr(), a_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(),
+                                  M, F, K, _act(wh, act), h.data_ptr(), out,
+                                  gate_up.data_ptr() if gate_up is not None else None,
+                                  _stream(stream, dev)), wh)
 
 
 def fp8q_grouped_gemm_gated(a_q, a_s, off, w_q, w_s, h, act="silu", gate_up=None, stream=None):
@@ -507,10 +540,12 @@ def fp8q_grouped_gemm_gated(a_q, a_s, off, w_q, w_s, h, act="silu", gate_up=None
     e's w_q[e][2F][K]; off is a device int32[G+1]."""
     wh = "fp8q_grouped_gemm_gated"
     _dims(wh, off, 1, "off")
-    M, F, K, out = _gated_args(wh, a_q, a_s, off, w_q, w_s, h, gate_up)
-    _invoke(lib.fp8q_grouped_gemm_gated, (_ptr(a_q), _ptr(a_s), M, _ptr(off), w_q.shape[0],
-                                          _ptr(w_q), _ptr(w_s), F, K, _act(wh, act), _ptr(h), out,
-                                          _ptr(gate_up), _stream(stream, a_q.device)), wh)
+    M, F, K, out, dev = _gated_args(wh, a_q, a_s, off, w_q, w_s, h, gate_up)
+    _invoke(lib.fp8q_grouped_gemm_gated, (a_q.data_ptr(), a_s.data_ptr(), M, off.data_ptr(),
+                                          w_q.shape[0], w_q.data_ptr(), w_s.data_ptr(), F, K,
+                                          _act(wh, act), h.data_ptr(), out,
+                                          gate_up.data_ptr() if gate_up is not None else None,
+                                          _stream(stream, dev)), wh)
 
 
 def fp8q_gated_backward(dh, gate_up, q, s, qt, st, act="silu", mode="f32", stream=None):
@@ -518,23 +553,25 @@ def fp8q_gated_backward(dh, gate_up, q, s, qt, st, act="silu", mode="f32", strea
     gate_up: bf16 [M][2F], quantized along the features (q: uint8 [M][2F], s:
     float32 [2F/128][M]) and along the tokens (qt: uint8 [2F][Mp], st: float32
     [Mp/128][2F], Mp = M up to a multiple of 128).  Either pair may be None."""
+    import torch
     wh = "fp8q_gated_backward"
     M, F = _dims(wh, dh, 2, "dh")
     _mult128(wh, F=F)
     dev = dh.device
-    _req(wh, "dh", dh, ["bf16"], (M, F), dev)
-    _req(wh, "gate_up", gate_up, ["bf16"], (M, 2 * F), dev)
+    _need(wh, dev, ("dh", dh, torch.bfloat16, (M, F)),
+          ("gate_up", gate_up, torch.bfloat16, (M, 2 * F)))
     if (q is None) != (s is None) or (qt is None) != (st is None) or (q is None and qt is None):
         raise ValueError(f"{wh}: codes and scales come in pairs, and one pair at least")
     if q is not None:
-        _req(wh, "q", q, ["u8"], (M, 2 * F), dev)
-        _req(wh, "s", s, ["f32"], (2 * F // GROUP, M), dev)
+        _need(wh, dev, ("q", q, torch.uint8, (M, 2 * F)),
+              ("s", s, torch.float32, (2 * F // GROUP, M)))
     if qt is not None:
         groups = -(-M // GROUP)
-        _req(wh, "qt", qt, ["u8"], (2 * F, groups * GROUP), dev)
-        _req(wh, "st", st, ["f32"], (groups, 2 * F), dev)
-    _invoke(lib.fp8q_gated_backward, (_ptr(dh), _ptr(gate_up), M, F, _act(wh, act), _MODES[mode],
-                                      _ptr(q), _ptr(s), _ptr(qt), _ptr(st),
+        _need(wh, dev, ("qt", qt, torch.uint8, (2 * F, groups * GROUP)),
+              ("st", st, torch.float32, (groups, 2 * F)))
+    _invoke(lib.fp8q_gated_backward, (dh.data_ptr(), gate_up.data_ptr(), M, F, _act(wh, act),
+                                      _MODES[mode], *(t.data_ptr() if t is not None else None
+                                                      for t in (q, s, qt, st)),
                                       _stream(stream, dev)), wh)
 
 
@@ -623,27 +660,29 @@ def quantize_token_i8(x, stream=None):
     """x: bf16 [M][K] -> (int8 codes [M][Kp], float32 scales [M]); Kp is K up to
     a multiple of 16, with zero codes past K."""
     import torch
-    M, K = _dims("quantize_token_i8", x, 2, "x")
+    wh = "fp8q_quantize_token_i8"
+    M, K = _dims(wh, x, 2, "x")
     q = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=x.device)
     s = torch.empty((M,), dtype=torch.float32, device=x.device)
-    fp8q_quantize_token_i8(x, q, s, stream)
+    _quantize_token_i8(wh, x, M, K, q, s, stream)
     return q, s
 
 
 def gemm_i8(a_q, a_s, w_q, w_s, bias=None, out_dtype=None, stream=None):
     import torch
-    c = torch.empty((a_q.shape[0], w_q.shape[0]), dtype=out_dtype or torch.float32,
-                    device=a_q.device)
-    fp8q_gemm_i8(a_q, a_s, w_q, w_s, c, bias, stream)
+    wh = "fp8q_gemm_i8"
+    c = torch.empty(_rows(wh, a_q, w_q), dtype=out_dtype or torch.float32, device=a_q.device)
+    _gemm_i8(wh, a_q, a_s, w_q, w_s, c, bias, stream)
     return c
 
 
 def gemm_i8_gated(a_q, a_s, w_q, w_s, act="silu", out_dtype=None, stream=None):
     """h = act(gate) * up (bfloat16 unless out_dtype says float32)."""
     import torch
-    h = torch.empty((a_q.shape[0], w_q.shape[0] // 2), dtype=out_dtype or torch.bfloat16,
-                    device=a_q.device)
-    fp8q_gemm_i8_gated(a_q, a_s, w_q, w_s, h, act, stream)
+    wh = "fp8q_gemm_i8_gated"
+    M, N = _rows(wh, a_q, w_q)
+    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
+    _gemm_i8_gated(wh, a_q, a_s, w_q, w_s, h, act, stream)
     return h
 
 

@@ -5,21 +5,31 @@
 //   E4M3:  Y[m][n] = sum_g a_s[g][m] w_s[n/128][g] sum_{k in chunk g} a[m][k] w[n][k]
 //   gated: h[m][f] = act(Y[m][f]) Y[m][F + f]
 //
-// At few rows the time is that of reading the weights, so nothing is shared
-// through LDS on the way in: a workgroup owns 16 weight rows (8 gate and the
-// 8 matching up rows when gated), its 8 waves split K in turns of 128, and a
-// lane loads its operand of the matrix instruction straight from memory, 16
-// bytes at a time.  4096 weight rows are then 256 workgroups, one for each CU,
-// with all of a 7168-long row block in flight at once.  The 8 partial sums meet
-// in LDS, in a fixed order; the int8 ones are exact in any order.
+// At few rows the time is that of reading the weights.  A workgroup owns 16
+// weight rows (8 gate and the 8 matching up rows when gated), so that 4096
+// weight rows are 256 workgroups, one for each CU; its 8 waves split K in turns
+// of 128.  A wave brings its chunks, of the weight and of the activation rows,
+// into a place of its own in LDS, 8 rows of 128 bytes a load, and waits for
+// nothing but its own loads; it asks for the next chunk as soon as the last one
+// is in registers, and the other waves cover the wait (rings of 2 to 4 chunks
+// a wave measured the same or slower: they leave room for fewer workgroups).
+// The 8 partial sums meet in LDS, in a fixed order; the int8 ones are exact in
+// any order.
 //
-// The activation rows are read again by every workgroup, from the L2: at 16
-// weight rows that is as many bytes as the weights for 16 activation rows,
-// which the L2 delivers beside the memory stream.
+// Loaded straight into registers, the operand layout of the matrix instruction
+// puts consecutive lanes on different rows, and the address unit takes a load's
+// 64 lanes one at a time: 16 bytes a clock and CU.  int8, 4096 x 7168 weights,
+// us for 1 / 16 / 32 / 64 rows: that way 6.9 / 8.7 / 11.6 / 18, through LDS 6.5
+// / 6.9 / 7.3 / 10.2, of which 3.6 is a launch that reads next to nothing; the
+// weights alone take 5.9 at the rate of a large copy.
+//
+// The activation rows are read again by every workgroup, from the L2: from 64
+// rows on that is most of what a CU loads, 80 bytes a ns.
 
 #include <type_traits>
 
 #include "activation.hpp"
+#include "gemm_common.hpp"
 
 namespace fp8q {
 
@@ -103,21 +113,21 @@ __device__ __forceinline__ bool find_rows(const int32_t* off, int G, int64_t M, 
   return true;
 }
 
-// One chunk's operands of a lane: bytes [16q, 16q+16) and [64+16q, 64+16q+16)
-// of the 128, for its weight row and its row of each activation block.
+// A lane offset past any block of rows, also with a scalar offset added.
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+// A wave's chunk in LDS: its 16 weight rows and its 16 MB activation rows.
 template <int MB>
-struct FewOperands {
-  v4i w[2];
-  v4i a[MB][2];
+struct FewCfg {
+  static constexpr int SLOT = 2048 * (1 + MB);
+  static constexpr int LDS = kFewWaves * SLOT;  // also holds the partial sums
 };
 
 template <int OP, int MB, bool GATED, bool GROUPED>
-__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const FewArgs p) {
+__device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
   constexpr int BM = 16 * MB;
-  constexpr int U = MB == 1 ? 4 : 2;  // chunks in a batch; two batches are in flight
   constexpr bool I8 = OP == kFewI8;
   using Acc = typename std::conditional<I8, v4i, v4f>::type;
-  __shared__ __attribute__((aligned(16))) float red[kFewWaves * MB * 256];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -137,93 +147,108 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const FewArgs p) 
     WS += I8 ? (int64_t)e * WR : (int64_t)e * (WR / 128) * KB;
   }
 
-  // this lane's weight row: row r16 of the block
+  // ---- loads: lane l of a load fetches row l/8 of its 8, physical piece l%8.
+  // Rows past the block's, and pieces past K, are out of the resource's range
+  // and come as zeros.
   constexpr int NCOL = GATED ? 8 : 16;  // output columns of the block
   const int64_t n0 = (int64_t)nb * NCOL;
-  int64_t col = n0 + (GATED ? (r16 & 7) : r16);
-  col = col < N ? col : N - 1;
-  const uint8_t* wp = W + (col + (GATED && r16 >= 8 ? N : 0)) * K + 16 * q;
-  const uint8_t* ap[MB];
+  const int live = __builtin_amdgcn_readfirstlane(r1 - r0 < BM ? (int)(r1 - r0) : BM);
+  const int cols = __builtin_amdgcn_readfirstlane(N - n0 < NCOL ? (int)(N - n0) : NCOL);
+  const int ks = (int)K;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + r0 * K, (int64_t)live * K);
+  // the first 8 weight rows and the second: gate and up rows when gated
+  const int second = GATED ? cols : cols > 8 ? cols - 8 : 0;
+  const __amdgpu_buffer_rsrc_t rw0 = make_rsrc(W + n0 * K, (int64_t)cols * K);
+  const __amdgpu_buffer_rsrc_t rw1 = make_rsrc(W + (n0 + (GATED ? N : 8)) * K, (int64_t)second * K);
+  const int pr = lane >> 3;
+  int kc[2];
+  uint32_t voff[2];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int64_t m = r0 + 16 * i + r16;
-    ap[i] = p.a + (m < r1 ? m : r1 - 1) * K + 16 * q;
+  for (int h = 0; h < 2; ++h) {
+    kc[h] = swz(8 * h + pr, lane & 7) * 16;  // its byte within the chunk
+    voff[h] = (uint32_t)(pr * ks + kc[h]);
   }
-
-  const int chunks = (int)((K + kFewChunk - 1) / kFewChunk);
-  const int mine = (chunks - wave + kFewWaves - 1) / kFewWaves;
-  // Chunk i of this wave.  Past the wave's last chunk, and for 16-byte pieces
-  // past K, the weights are read from the row's start and the activations
-  // taken as zero.
-  auto load = [&](FewOperands<MB>& o, int i) {
-    const int64_t k = ((int64_t)i * kFewWaves + wave) * kFewChunk;
+  uint8_t* const mine = smem + wave * FewCfg<MB>::SLOT;
+  auto load = [&](int k) {
+    uint32_t v[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t kh = k + 64 * h;
-      const bool in = i < mine && kh + 16 * q < K;
-      const int64_t ks = in ? kh : 0;
-      o.w[h] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(in ? wp + kh : wp - 16 * q));
+    for (int h = 0; h < 2; ++h) v[h] = k + kc[h] < ks ? voff[h] : kOutOfRange;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw0, to_lds(mine), 16, v[0], k, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw1, to_lds(mine + 1024), 16, v[1], k, 0, 0);
 #pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        o.a[b][h] = *reinterpret_cast<const v4i*>(in ? ap[b] + ks : ap[b] - 16 * q);
-        if (!in) o.a[b][h] = v4i{0, 0, 0, 0};
-      }
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to_lds(mine + 2048 * (1 + b) + 1024 * h), 16,
+                                                 v[h], k + (16 * b + 8 * h) * ks, 0, 0);
+  };
+  // E4M3: the scales of chunk g for this lane's results: its activation rows',
+  // and of its 4 weight rows, which lie in one block row (F is a multiple of 128)
+  float s_a[MB], s_w = 0.f;
+  const float *sa_at = nullptr, *sw_at = nullptr;
+  if constexpr (!I8) {
+    sa_at = p.a_s + r0;
+    sw_at = WS + (n0 + (GATED && q >= 2 ? N : 0)) / 128 * KB;
+  }
+  auto load_scales = [&](int g) {
+    const int64_t gs = g < KB ? g : 0;  // past the end the products are zeros
+    s_w = sw_at[gs];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int m = 16 * b + r16;
+      s_a[b] = sa_at[gs * p.M + (m < live ? m : live - 1)];
     }
   };
 
   Acc acc[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b] = Acc{0, 0, 0, 0};
-  // E4M3: the scales of this lane's 4 results, which share one activation row
-  // and (F is a multiple of 128) one weight block row
-  const float* sw = nullptr;
-  const float* sa = nullptr;
-  if constexpr (!I8) {
-    const int64_t blk_row = GATED ? n0 + (q >= 2 ? N : 0) : n0;
-    sw = WS + blk_row / 128 * KB;
-    sa = p.a_s;
-  }
-  auto multiply = [&](const FewOperands<MB>& o, int i) {
+  const int chunks = (int)((K + kFewChunk - 1) / kFewChunk);
+  load(wave * kFewChunk);
+  if constexpr (!I8) load_scales(wave);
+  for (int g = wave; g < chunks; g += kFewWaves) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    v4i w[2], a[MB][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = *reinterpret_cast<const v4i*>(mine + r16 * 128 + swz(r16, q + 4 * h) * 16);
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        a[b][h] = *reinterpret_cast<const v4i*>(mine + 2048 * (1 + b) + r16 * 128 +
+                                                swz(r16, q + 4 * h) * 16);
+    float s[MB];
+    if constexpr (!I8) {
+#pragma unroll
+      for (int b = 0; b < MB; ++b) s[b] = s_a[b] * s_w;
+    }
+    // the chunk is in registers: ask for the next one
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load((g + kFewWaves) * kFewChunk);
+    if constexpr (!I8) load_scales(g + kFewWaves);
     if constexpr (I8) {
 #pragma unroll
       for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(o.w[h], o.a[b][h], acc[b], 0, 0, 0);
+          acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], a[b][h], acc[b], 0, 0, 0);
     } else {
-      const int g = i * kFewWaves + wave;
-      const int gs = i < mine ? g : 0;  // past the end the partial is zero
-      const float s_w = sw[gs];
-      const v8i w = {o.w[0][0], o.w[0][1], o.w[0][2], o.w[0][3],
-                     o.w[1][0], o.w[1][1], o.w[1][2], o.w[1][3]};
+      const v8i wf = {w[0][0], w[0][1], w[0][2], w[0][3], w[1][0], w[1][1], w[1][2], w[1][3]};
 #pragma unroll
       for (int b = 0; b < MB; ++b) {
-        const v8i a = {o.a[b][0][0], o.a[b][0][1], o.a[b][0][2], o.a[b][0][3],
-                       o.a[b][1][0], o.a[b][1][1], o.a[b][1][2], o.a[b][1][3]};
+        const v8i af = {a[b][0][0], a[b][0][1], a[b][0][2], a[b][0][3],
+                        a[b][1][0], a[b][1][1], a[b][1][2], a[b][1][3]};
         const v4f P = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            w, a, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-        const int64_t m = r0 + 16 * b + r16;
-        const float s = sa[(int64_t)gs * p.M + (m < r1 ? m : r1 - 1)] * s_w;
+            wf, af, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[b][j] = __builtin_fmaf(P[j], s, acc[b][j]);
+        for (int j = 0; j < 4; ++j) acc[b][j] = __builtin_fmaf(P[j], s[b], acc[b][j]);
       }
     }
-  };
-
-  FewOperands<MB> x[U], y[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) load(x[u], u);
-  for (int i = 0; i < mine; i += 2 * U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(y[u], i + U + u);
-#pragma unroll
-    for (int u = 0; u < U; ++u) multiply(x[u], i + u);
-    if (i + U >= mine) break;
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(x[u], i + 2 * U + u);
-#pragma unroll
-    for (int u = 0; u < U; ++u) multiply(y[u], i + U + u);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();  // every wave is done with its chunks
+  float* const red = reinterpret_cast<float*>(smem);
 
   // partial sums: red[wave][block][lane][4]
 #pragma unroll
@@ -278,18 +303,25 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const FewArgs p) 
   }
 }
 
+template <int OP, int MB, bool GATED, bool GROUPED>
+__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const FewArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[FewCfg<MB>::LDS];
+  few_rows<OP, MB, GATED, GROUPED>(p, smem);
+}
+
 template <int OP, bool GATED, bool GROUPED>
 static hipError_t launch_few(FewArgs p, int64_t row_blocks_extra, hipStream_t stream) {
   constexpr int NCOL = GATED ? 8 : 16;
   const int64_t n_blocks = (p.N + NCOL - 1) / NCOL;
-  const int MB = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-  // by expert: sum_e ceil(M_e / BM) <= floor(M / BM) + G
+  const int MB = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 4 : 8;
+  // (by expert: sum_e ceil(M_e / BM) <= floor(M / BM) + G)
   const int64_t m_blocks = (p.M + 16 * MB - 1) / (16 * MB) + row_blocks_extra;
   if (n_blocks * m_blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   p.n_blocks = (int)n_blocks;
   auto kern = MB == 1   ? few_rows_kernel<OP, 1, GATED, GROUPED>
               : MB == 2 ? few_rows_kernel<OP, 2, GATED, GROUPED>
-                        : few_rows_kernel<OP, 4, GATED, GROUPED>;
+              : MB == 4 ? few_rows_kernel<OP, 4, GATED, GROUPED>
+                        : few_rows_kernel<OP, 8, GATED, GROUPED>;
   hipLaunchKernelGGL(kern, dim3((unsigned)(n_blocks * m_blocks)), dim3(kFewThreads), 0, stream, p);
   return hipGetLastError();
 }

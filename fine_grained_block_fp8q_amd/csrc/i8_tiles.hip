@@ -293,7 +293,6 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
   uint8_t* const rows = mine + Cfg::WN * 8;
   const int64_t nw = n0 + wave_n * Cfg::WNO;  // the wave's first output column
   const int live_n = (int)(p.N - nw < Cfg::WNO ? (p.N - nw > 0 ? p.N - nw : 0) : Cfg::WNO);
-  const bool vec = (p.N * OB) % 16 == 0;  // every row of C starts at a 16-byte boundary
   // As many row blocks at a time as the wave's share holds, then one loop that
   // stores them: the code runs once a tile, and what it costs is to fetch it.
   constexpr int NO = Cfg::WNO / 16, IB = Cfg::ROW_BLOCKS;
@@ -329,24 +328,18 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
       }
     lds_wave_fence();
     const int live_m = (int)(p.M - mb < 16 * IB ? (p.M - mb > 0 ? p.M - mb : 0) : 16 * IB);
-    if (vec) {
+    // (rows of an odd N start anywhere: the stores are then unaligned ones)
 #pragma unroll 4
-      for (int x = lane; x < 16 * IB * PER; x += 64) {
-        const int r = x / PER, c = x % PER;
-        if (r < live_m && c * 16 < live_n * OB)
-          *reinterpret_cast<v4u*>(static_cast<uint8_t*>(p.c) + ((mb + r) * p.N + nw) * OB + c * 16) =
-              *reinterpret_cast<const v4u*>(rows + r * PITCH + c * 16);
-      }
-    } else {
-      for (int x = lane; x < 16 * IB * Cfg::WNO; x += 64) {
-        const int r = x / Cfg::WNO, c = x % Cfg::WNO;
-        if (r < live_m && c < live_n) {
-          const int64_t at = (mb + r) * p.N + nw + c;
-          if constexpr (Cfg::BF16)
-            static_cast<uint16_t*>(p.c)[at] = *reinterpret_cast<const uint16_t*>(rows + r * PITCH + c * 2);
-          else
-            static_cast<float*>(p.c)[at] = *reinterpret_cast<const float*>(rows + r * PITCH + c * 4);
-        }
+    for (int x = lane; x < 16 * IB * PER; x += 64) {
+      const int r = x / PER, c = x % PER, left = live_n * OB - c * 16;
+      if (r >= live_m || left <= 0) continue;
+      const uint8_t* from = rows + r * PITCH + c * 16;
+      uint8_t* to = static_cast<uint8_t*>(p.c) + ((mb + r) * p.N + nw) * OB + c * 16;
+      if (left >= 16) {
+        const v4u v = *reinterpret_cast<const v4u*>(from);
+        __builtin_memcpy(to, &v, 16);
+      } else {
+        for (int e = 0; e < left; e += OB) __builtin_memcpy(to + e, from + e, OB);
       }
     }
     lds_wave_fence();
@@ -403,12 +396,55 @@ hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                          const float* bias, int64_t M, int64_t N, int64_t K, bool gated, int act,
                          void* c, int out_bf16, hipStream_t stream);
 
+// Which kernel serves M x N x K (weight_rows = N, or 2F when gated): the one
+// that the following estimate of its time in ns gives least for.  c: a CU's
+// time for 128 k of one workgroup's tile with every CU at work; e: its
+// epilogue.  Measured with 4096 weight rows, K = 7168, in us:
+//   rows          64    128   256   512   1024  2048  4096
+//   few rows      10.2  15.8  29
+//   64 x 128      19.6  19.7  20.1  22.6  39    76
+//   128 x 128     23.6  24.7  24.9  25.8  33    57    108
+//   256 x 256           68    68    69    69    72    90
+static int pick_i8(int64_t M, int64_t weight_rows, int64_t K, int cus) {
+  auto blocks = [](int64_t x, int64_t b) { return (x + b - 1) / b; };
+  const int64_t chunks = blocks(K, 128);
+  if (M <= 32) return 0;
+  struct Variant {
+    int tile, bm, bn;
+    double c, e;
+  };
+  // few rows: (16 + rows) * 128 bytes a chunk at 80 bytes a ns
+  const int fm = M <= 64 ? 64 : 128;
+  const Variant variants[] = {{0, fm, 16, (16 + fm) * 1.6, 0.0},
+                              {64, 64, 128, 310.0, 600.0},
+                              {128, 128, 128, 480.0, 1200.0},
+                              {256, 256, 256, 1420.0, 6000.0}};
+  int best = 0;
+  double least = 1e300;
+  for (const Variant& v : variants) {
+    const int64_t n = blocks(M, v.bm) * blocks(weight_rows, v.bn);
+    // a tile's chunk takes about 3/4 of that when most CUs are idle
+    const double c = n * 2 < cus && v.tile ? 0.75 * v.c : v.c;
+    const double t = (double)blocks(n, cus) * ((double)chunks * c + v.e);
+    if (t < least) {
+      least = t;
+      best = v.tile;
+    }
+  }
+  return best;
+}
+
 static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                             const float* w_s, const float* bias, int64_t M, int64_t N, int64_t K,
                             bool gated, int act, void* c, int out_bf16, hipStream_t stream) {
-  if (M <= 64)
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+    return hipGetLastError();
+  const int tile = pick_i8(M, gated ? 2 * N : N, K, cus);
+  if (tile == 0)
     return launch_i8_few(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, stream);
-  return launch_i8_tiles(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, 256, stream);
+  return launch_i8_tiles(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, tile, stream);
 }
 
 hipError_t launch_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
