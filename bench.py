@@ -664,7 +664,8 @@ def setup_grouped(fq, torch, name, sets, fused=False, precise=False):
 
 
 # -------------------------------------------------------- recorded traffic
-GEMM_SOURCES = ("gemm_kernels.hip", "gemm_common.hpp", "fp8q_device.hpp", "quant_rules.hpp")
+GEMM_SOURCES = ("gemm_kernels.hip", "gemm_tile.hpp", "grouped_gemm.hpp", "gemm_common.hpp",
+                "fp8q_device.hpp", "quant_rules.hpp")
 
 
 def kernel_source_digest():

@@ -44,6 +44,8 @@ SOURCES = {
     # (left rolled, its register arrays would go to scratch memory)
     "gemm_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1",
                          "-mllvm", "-pragma-unroll-threshold=60000"],
+    "gated_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1",
+                       "-mllvm", "-pragma-unroll-threshold=60000"],
     "token_quant.hip": ["-ffp-contract=off"],
     "few_rows.hip": [],
     "i8_tiles.hip": [],

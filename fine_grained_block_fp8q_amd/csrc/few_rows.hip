@@ -41,77 +41,15 @@ constexpr int kFewChunk = 128;  // K of one wave's turn
 struct FewArgs {
   const uint8_t* a;
   const float* a_s;    // int8: [M]; E4M3: [K/128][M]
-  const uint8_t* w;    // [N][K] or [G][2F][K]
+  const uint8_t* w;    // [N][K], or [2F][K] when gated
   const float* w_s;    // int8: [N]; E4M3: [N/128][K/128]
   const float* bias;   // int8, not gated: [N] or NULL
-  const int32_t* off;  // by expert: [G + 1], else NULL
   void* c;             // [M][N], or h [M][F]
   uint16_t* gu;        // gated: Y as BF16 [M][2F], or NULL
   int64_t M, N, K;     // N: output columns (F when gated)
-  int G;
   int n_blocks;        // column blocks
   int out_bf16, act;
 };
-
-#ifdef FP8Q_DEBUG_CHECKS
-// Set by a launch by expert that found invalid offsets (debug builds): read
-// and cleared by the host entry point after its synchronization.
-__device__ int g_gated_offsets_error = 0;
-
-hipError_t gated_offsets_error_take(hipStream_t stream, int* flag) {
-  const int zero = 0;
-  hipError_t e = hipMemcpyFromSymbolAsync(flag, HIP_SYMBOL(g_gated_offsets_error), sizeof(int), 0,
-                                          hipMemcpyDeviceToHost, stream);
-  if (e == hipSuccess) e = hipStreamSynchronize(stream);
-  if (e == hipSuccess && *flag)
-    e = hipMemcpyToSymbol(HIP_SYMBOL(g_gated_offsets_error), &zero, sizeof(int), 0,
-                          hipMemcpyHostToDevice);
-  return e;
-}
-#endif
-
-// Rows of block `y` of BM rows when rows are grouped by expert: the expert's
-// blocks follow those of the experts before it.  Every lane gets the same
-// answer.  False where there is no such block, or the offsets are not
-// 0 = off[0] <= ... <= off[G] <= M (then no block has any: nothing is written).
-__device__ __forceinline__ bool find_rows(const int32_t* off, int G, int64_t M, int BM, int y,
-                                          int& e, int64_t& r0, int64_t& r1) {
-  const int lane = threadIdx.x & 63;
-  bool bad = lane == 0 && (off[0] != 0 || (int64_t)off[G] > M);
-  int before = 0, at = -1, lo_at = 0, hi_at = 0, blk = 0;
-  for (int base = 0; base < G; base += 64) {
-    const int i = base + lane;
-    const int lo = i < G ? off[i] : 0, hi = i < G ? off[i + 1] : 0;
-    bad = bad || hi < lo;
-    const int n = hi > lo ? (hi - lo + BM - 1) / BM : 0;
-    int inc = n;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(inc, d);
-      if (lane >= d) inc += v;
-    }
-    const int first = before + inc - n;
-    const uint64_t hit = __ballot(y >= first && y < first + n);
-    if (hit != 0) {
-      const int l = __builtin_ctzll(hit);
-      at = base + l;
-      lo_at = __shfl(lo, l);
-      hi_at = __shfl(hi, l);
-      blk = y - __shfl(first, l);
-    }
-    before += __shfl(inc, 63);
-  }
-  if (__ballot(bad) != 0) {
-#ifdef FP8Q_DEBUG_CHECKS
-    if (blockIdx.x == 0 && threadIdx.x == 0) g_gated_offsets_error = 1;
-#endif
-    return false;
-  }
-  if (at < 0) return false;
-  e = __builtin_amdgcn_readfirstlane(at);
-  r0 = lo_at + (int64_t)blk * BM;
-  r1 = hi_at;
-  return true;
-}
 
 // A lane offset past any block of rows, also with a scalar offset added.
 constexpr uint32_t kOutOfRange = 0x80000000u;
@@ -123,7 +61,7 @@ struct FewCfg {
   static constexpr int LDS = kFewWaves * SLOT;  // also holds the partial sums
 };
 
-template <int OP, int MB, bool GATED, bool GROUPED>
+template <int OP, int MB, bool GATED>
 __device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
   constexpr int BM = 16 * MB;
   constexpr bool I8 = OP == kFewI8;
@@ -134,32 +72,23 @@ __device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
   const int r16 = lane & 15, q = lane >> 4;
   const int nb = blockIdx.x % p.n_blocks, mb = blockIdx.x / p.n_blocks;
 
-  int64_t r0 = (int64_t)mb * BM, r1 = p.M;
-  const uint8_t* W = p.w;
-  const float* WS = p.w_s;
+  const int64_t r0 = (int64_t)mb * BM;
   const int64_t K = p.K, N = p.N;
-  const int64_t WR = GATED ? 2 * N : N;  // weight rows
-  const int64_t KB = K / kFewChunk;      // E4M3: whole chunks
-  if constexpr (GROUPED) {
-    int e;
-    if (!find_rows(p.off, p.G, p.M, BM, mb, e, r0, r1)) return;
-    W += (int64_t)e * WR * K;
-    WS += I8 ? (int64_t)e * WR : (int64_t)e * (WR / 128) * KB;
-  }
+  const int64_t KB = K / kFewChunk;  // E4M3: whole chunks
 
   // ---- loads: lane l of a load fetches row l/8 of its 8, physical piece l%8.
   // Rows past the block's, and pieces past K, are out of the resource's range
   // and come as zeros.
   constexpr int NCOL = GATED ? 8 : 16;  // output columns of the block
   const int64_t n0 = (int64_t)nb * NCOL;
-  const int live = __builtin_amdgcn_readfirstlane(r1 - r0 < BM ? (int)(r1 - r0) : BM);
+  const int live = __builtin_amdgcn_readfirstlane(p.M - r0 < BM ? (int)(p.M - r0) : BM);
   const int cols = __builtin_amdgcn_readfirstlane(N - n0 < NCOL ? (int)(N - n0) : NCOL);
   const int ks = (int)K;
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + r0 * K, (int64_t)live * K);
   // the first 8 weight rows and the second: gate and up rows when gated
   const int second = GATED ? cols : cols > 8 ? cols - 8 : 0;
-  const __amdgpu_buffer_rsrc_t rw0 = make_rsrc(W + n0 * K, (int64_t)cols * K);
-  const __amdgpu_buffer_rsrc_t rw1 = make_rsrc(W + (n0 + (GATED ? N : 8)) * K, (int64_t)second * K);
+  const __amdgpu_buffer_rsrc_t rw0 = make_rsrc(p.w + n0 * K, (int64_t)cols * K);
+  const __amdgpu_buffer_rsrc_t rw1 = make_rsrc(p.w + (n0 + (GATED ? N : 8)) * K, (int64_t)second * K);
   const int pr = lane >> 3;
   int kc[2];
   uint32_t voff[2];
@@ -188,7 +117,7 @@ __device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
   const float *sa_at = nullptr, *sw_at = nullptr;
   if constexpr (!I8) {
     sa_at = p.a_s + r0;
-    sw_at = WS + (n0 + (GATED && q >= 2 ? N : 0)) / 128 * KB;
+    sw_at = p.w_s + (n0 + (GATED && q >= 2 ? N : 0)) / 128 * KB;
   }
   auto load_scales = [&](int g) {
     const int64_t gs = g < KB ? g : 0;  // past the end the products are zeros
@@ -279,13 +208,13 @@ __device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
   for (int i = tid; i < BM * NCOL; i += kFewThreads) {
     const int m = i / NCOL, c = i % NCOL;
     const int64_t row = r0 + m, n = n0 + c;
-    if (row >= r1 || n >= N) continue;
+    if (row >= p.M || n >= N) continue;
     if constexpr (GATED) {
       float g, u;
       if constexpr (I8) {
         const float s = p.a_s[row];
-        g = (float)total(m, c) * s * WS[n];
-        u = (float)total(m, c + 8) * s * WS[N + n];
+        g = (float)total(m, c) * s * p.w_s[n];
+        u = (float)total(m, c + 8) * s * p.w_s[N + n];
       } else {
         g = total(m, c);
         u = total(m, c + 8);
@@ -296,32 +225,31 @@ __device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
         store(p.gu, row * 2 * N + N + n, u, 1);
       }
     } else {
-      float v = (float)total(m, c) * p.a_s[row] * WS[n];
+      float v = (float)total(m, c) * p.a_s[row] * p.w_s[n];
       if (p.bias) v += p.bias[n];
       store(p.c, row * N + n, v, p.out_bf16);
     }
   }
 }
 
-template <int OP, int MB, bool GATED, bool GROUPED>
+template <int OP, int MB, bool GATED>
 __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const FewArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[FewCfg<MB>::LDS];
-  few_rows<OP, MB, GATED, GROUPED>(p, smem);
+  few_rows<OP, MB, GATED>(p, smem);
 }
 
-template <int OP, bool GATED, bool GROUPED>
-static hipError_t launch_few(FewArgs p, int64_t row_blocks_extra, hipStream_t stream) {
+template <int OP, bool GATED>
+static hipError_t launch_few(FewArgs p, hipStream_t stream) {
   constexpr int NCOL = GATED ? 8 : 16;
   const int64_t n_blocks = (p.N + NCOL - 1) / NCOL;
   const int MB = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 4 : 8;
-  // (by expert: sum_e ceil(M_e / BM) <= floor(M / BM) + G)
-  const int64_t m_blocks = (p.M + 16 * MB - 1) / (16 * MB) + row_blocks_extra;
+  const int64_t m_blocks = (p.M + 16 * MB - 1) / (16 * MB);
   if (n_blocks * m_blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   p.n_blocks = (int)n_blocks;
-  auto kern = MB == 1   ? few_rows_kernel<OP, 1, GATED, GROUPED>
-              : MB == 2 ? few_rows_kernel<OP, 2, GATED, GROUPED>
-              : MB == 4 ? few_rows_kernel<OP, 4, GATED, GROUPED>
-                        : few_rows_kernel<OP, 8, GATED, GROUPED>;
+  auto kern = MB == 1   ? few_rows_kernel<OP, 1, GATED>
+              : MB == 2 ? few_rows_kernel<OP, 2, GATED>
+              : MB == 4 ? few_rows_kernel<OP, 4, GATED>
+                        : few_rows_kernel<OP, 8, GATED>;
   hipLaunchKernelGGL(kern, dim3((unsigned)(n_blocks * m_blocks)), dim3(kFewThreads), 0, stream, p);
   return hipGetLastError();
 }
@@ -341,21 +269,18 @@ hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q,
   p.K = K;
   p.act = act;
   p.out_bf16 = out_bf16;
-  return gated ? launch_few<kFewI8, true, false>(p, 0, stream)
-               : launch_few<kFewI8, false, false>(p, 0, stream);
+  return gated ? launch_few<kFewI8, true>(p, stream)
+               : launch_few<kFewI8, false>(p, stream);
 }
 
-// off NULL: one dense block of weights; else G experts.
-hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, const int32_t* off,
-                             int G, const uint8_t* w_q, const float* w_s, int64_t F, int64_t K,
-                             int act, void* h, int out_bf16, void* gu, hipStream_t stream) {
+hipError_t launch_gated_few(const uint8_t* a_q, const float* a_s, int64_t M, const uint8_t* w_q,
+                            const float* w_s, int64_t F, int64_t K, int act, void* h, int out_bf16,
+                            void* gu, hipStream_t stream) {
   FewArgs p{};
   p.a = a_q;
   p.a_s = a_s;
   p.w = w_q;
   p.w_s = w_s;
-  p.off = off;
-  p.G = G;
   p.c = h;
   p.gu = static_cast<uint16_t*>(gu);
   p.M = M;
@@ -363,8 +288,7 @@ hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, co
   p.K = K;
   p.act = act;
   p.out_bf16 = out_bf16;
-  if (off) return launch_few<kFewE4M3, true, true>(p, G, stream);
-  return launch_few<kFewE4M3, true, false>(p, 0, stream);
+  return launch_few<kFewE4M3, true>(p, stream);
 }
 
 }  // namespace fp8q

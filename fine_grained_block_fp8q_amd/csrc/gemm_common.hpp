@@ -41,13 +41,15 @@ struct TileArgs {
   int64_t a_row0;       // first A row of the tile
   int64_t a_rows;       // exclusive end of the valid A rows
   int64_t w_row0;       // first W row (= output column) of the tile
-  int64_t w_rows;       // N
+  int64_t w_rows;       // N (gated: F, with the up rows behind the gate rows)
   int64_t K;
   int64_t sa_ld;        // leading dimension of SA (total rows)
   int64_t sw_ld;        // row-scaled weight operand: leading dimension of SW = [K/128][sw_ld]
   void* C;              // output base
   int64_t ldc;          // N
   int out_bf16;
+  uint16_t* gu;         // gated: Y as BF16 [a rows][2 ldc], or NULL
+  int act;              // gated: activation
 };
 
 // Buffer resource over [base, base + bytes) for raw loads (gfx9 word 3:

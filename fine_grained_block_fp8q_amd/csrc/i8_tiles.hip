@@ -31,6 +31,7 @@
 
 #include "activation.hpp"
 #include "gemm_common.hpp"
+#include "tile_choice.hpp"
 
 namespace fp8q {
 
@@ -396,43 +397,15 @@ hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                          const float* bias, int64_t M, int64_t N, int64_t K, bool gated, int act,
                          void* c, int out_bf16, hipStream_t stream);
 
-// Which kernel serves M x N x K (weight_rows = N, or 2F when gated): the one
-// that the following estimate of its time in ns gives least for.  c: a CU's
-// time for 128 k of one workgroup's tile with every CU at work; e: its
-// epilogue.  Measured with 4096 weight rows, K = 7168, in us:
+// Kernel times with 4096 weight rows, K = 7168, in us, by number of rows:
 //   rows          64    128   256   512   1024  2048  4096
 //   few rows      10.2  15.8  29
 //   64 x 128      19.6  19.7  20.1  22.6  39    76
 //   128 x 128     23.6  24.7  24.9  25.8  33    57    108
 //   256 x 256           68    68    69    69    72    90
-static int pick_i8(int64_t M, int64_t weight_rows, int64_t K, int cus) {
-  auto blocks = [](int64_t x, int64_t b) { return (x + b - 1) / b; };
-  const int64_t chunks = blocks(K, 128);
-  if (M <= 32) return 0;
-  struct Variant {
-    int tile, bm, bn;
-    double c, e;
-  };
-  // few rows: (16 + rows) * 128 bytes a chunk at 80 bytes a ns
-  const int fm = M <= 64 ? 64 : 128;
-  const Variant variants[] = {{0, fm, 16, (16 + fm) * 1.6, 0.0},
-                              {64, 64, 128, 310.0, 600.0},
-                              {128, 128, 128, 480.0, 1200.0},
-                              {256, 256, 256, 1420.0, 6000.0}};
-  int best = 0;
-  double least = 1e300;
-  for (const Variant& v : variants) {
-    const int64_t n = blocks(M, v.bm) * blocks(weight_rows, v.bn);
-    // a tile's chunk takes about 3/4 of that when most CUs are idle
-    const double c = n * 2 < cus && v.tile ? 0.75 * v.c : v.c;
-    const double t = (double)blocks(n, cus) * ((double)chunks * c + v.e);
-    if (t < least) {
-      least = t;
-      best = v.tile;
-    }
-  }
-  return best;
-}
+constexpr TileVariant kI8Variants[] = {{64, 64, 128, 273, 325, 625, 800},
+                                       {128, 128, 128, 350, 496, 932, 1600},
+                                       {256, 256, 256, 1027, 1375, 2750, 7000}};
 
 static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                             const float* w_s, const float* bias, int64_t M, int64_t N, int64_t K,
@@ -441,7 +414,7 @@ static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
     return hipGetLastError();
-  const int tile = pick_i8(M, gated ? 2 * N : N, K, cus);
+  const int tile = pick_variant(kI8Variants, M, gated ? 2 * N : N, (K + 127) / 128, cus);
   if (tile == 0)
     return launch_i8_few(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, stream);
   return launch_i8_tiles(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, tile, stream);
