@@ -499,6 +499,7 @@ fp8q_status fp8q_gated_backward(const void* dh, const void* gate_up, int64_t M, 
     return FP8Q_ERR_ALIGN;
   if (!valid_act(act) || !valid_mode(mode)) return FP8Q_ERR_ENUM;
   if (empty) return FP8Q_OK;
+  if (F > (int64_t(1) << 22)) return FP8Q_ERR_UNSUPPORTED;  // 32-bit offsets within 128 tokens
   const fp8q_status d = check_device();
   if (d != FP8Q_OK) return d;
   return launched(fp8q::launch_gated_backward(dh, gate_up, M, F, act, mode, q, s, qt, st, stream));

@@ -12,14 +12,25 @@
 // whole groups in both directions.  Lane (rq = t/16, l16 = t%16) owns tokens
 // 4rq .. 4rq+3 at features 8 l16 .. 8 l16 + 7.  A row group's maximum is one
 // DPP row's; a column group's goes over the lane's 4 tokens, the wave's 4 rq
-// (shuffles) and the 8 waves (LDS).  The lane's 4 tokens of one feature are one
-// word of the transposed codes, which are gathered in LDS and stored 128 bytes
-// (a feature's group of tokens) to 8 lanes.
+// (shuffles) and the 8 waves (LDS).  Each group's rule (two divisions) is
+// worked out by one lane, not by all that hold the group: lane i of a DPP row
+// takes row group i of its 8 and broadcasts the multiplier.  The lane's 4
+// tokens of one feature are one word of the transposed codes, which are
+// gathered in LDS and stored 128 bytes (a feature's group of tokens) to 8 lanes.
+//
+// 4000 tokens, F = 2048: 16.2 us for 82 MB (5.1 TB/s, a large copy's rate); the
+// rows' form alone 12.4, the tokens' alone 14.1.  With the library's exponential,
+// correctly rounded divisions by every lane and branches for the last tokens it
+// was 22.2, bound by the vector ALU.  A single workgroup takes 5 us of its 1580
+// vector instructions: what small batches cost beside the launch.
 //
 // Tokens past M count as zeros: the last group of tokens is a full one, and its
 // codes past M are zero.
 
+#include <type_traits>
+
 #include "activation.hpp"
+#include "gemm_common.hpp"
 #include "quant_rules.hpp"
 
 namespace fp8q {
@@ -34,6 +45,13 @@ __device__ __forceinline__ float bf16_elem(const uint4& v, int j) {
   return (j & 1) ? bf16_hi(w) : bf16_lo(w);
 }
 
+constexpr int kNonTemporal = 2;  // cache policy bit of a buffer store
+
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  const v4u v = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // LDS byte of token word rq (tokens 4rq..4rq+3) of feature c in a transposed
 // tile: rows of 128 bytes whose 16-byte pieces are exchanged by the feature's
 // octet, so that the 16 l16 of a wave write 8 different pieces.
@@ -41,31 +59,67 @@ __device__ __forceinline__ int tile_at(int c, int rq) {
   return c * 128 + (((rq >> 2) ^ (c >> 3)) & 7) * 16 + (rq & 3) * 4;
 }
 
+// What apply() needs of a rule, in 32 bits: the multiplier or the exponent.
 template <int MODE>
-__global__ __launch_bounds__(kBwThreads) void gated_backward_kernel(
-    const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu, int64_t M, int64_t F, int act,
-    uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
-    float* __restrict__ st, int64_t Mp, int n_fblk) {
-  __shared__ float colmax[8][2][128];
-  __shared__ GroupRule colrule[2][128];
-  __shared__ __attribute__((aligned(16))) uint8_t tile[2][128 * 128];
+__device__ __forceinline__ float rule_word(const GroupRule& r) {
+  return MODE == 0 ? r.mul : __int_as_float(r.neg_e);
+}
+template <int MODE>
+__device__ __forceinline__ GroupRule word_rule(float w) {
+  GroupRule r;
+  r.mul = MODE == 0 ? w : 0.f;
+  r.neg_e = MODE == 0 ? 0 : __float_as_int(w);
+  r.s = 0.f;
+  return r;
+}
+
+// The rule that lane N of this DPP row (16 lanes) holds.
+template <int MODE, int N>
+__device__ __forceinline__ GroupRule rule_of_lane(const GroupRule& r) {
+  constexpr int kRowNewBcast = 0x150;
+  return word_rule<MODE>(__int_as_float(__builtin_amdgcn_update_dpp(
+      0, __float_as_int(rule_word<MODE>(r)), kRowNewBcast + N, 0xF, 0xF, false)));
+}
+
+// max(m, |a|, |b|), one instruction (written with fmaxf each operand is first
+// made a quiet number by one of its own).
+__device__ __forceinline__ float max3abs(float m, float a, float b) {
+  float r;
+  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(m), "v"(a), "v"(b));
+  return r;
+}
+
+struct BwShared {
+  float colmax[8][2][128];
+  float colmul[2][128];  // a column's multiplier (16-byte aligned)
+  uint8_t tile[2][128 * 128];
+};
+
+template <int MODE, int ACT>
+__device__ __forceinline__ void gated_backward(
+    const uint16_t* dh, const uint16_t* gu, int64_t M, int64_t F, uint8_t* q, float* s, uint8_t* qt,
+    float* st, int64_t Mp, int n_fblk, BwShared& sh) {
   const int fb = blockIdx.x % n_fblk;
   const int64_t tb = blockIdx.x / n_fblk;
   const int t = threadIdx.x, l16 = t & 15, rq = t >> 4, wave = t >> 6;
   const int64_t m0 = tb * kGroup + 4 * rq;
   const int64_t f0 = (int64_t)fb * kGroup + 8 * l16;
 
+  // Byte offsets within the block's 128 tokens; of tokens past M loads deliver
+  // zeros and stores are dropped (they are out of the resources' range).
+  const int64_t mb = tb * kGroup;
+  const int live = __builtin_amdgcn_readfirstlane(M - mb < kGroup ? (int)(M - mb) : kGroup);
+  const __amdgpu_buffer_rsrc_t rd = make_rsrc(dh + mb * F, live * F * 2);
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(gu + mb * 2 * F, live * F * 4);
+  const int fs = (int)F;
   uint4 vd[4], vg[4], vu[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + i;
-    if (m < M) {
-      vd[i] = *reinterpret_cast<const uint4*>(dh + m * F + f0);
-      vg[i] = *reinterpret_cast<const uint4*>(gu + m * 2 * F + f0);
-      vu[i] = *reinterpret_cast<const uint4*>(gu + m * 2 * F + F + f0);
-    } else {
-      vd[i] = vg[i] = vu[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
+    const int r = 4 * rq + i;
+    const uint32_t at = (uint32_t)(r * fs + (int)f0) * 2, aty = at + (uint32_t)(r * fs) * 2;
+    vd[i] = load16(rd, at);
+    vg[i] = load16(ry, aty);
+    vu[i] = load16(ry, aty + (uint32_t)fs * 2);
   }
   float d[2][4][8];  // dgate, dup
 #pragma unroll
@@ -74,31 +128,47 @@ __global__ __launch_bounds__(kBwThreads) void gated_backward_kernel(
     for (int j = 0; j < 8; ++j) {
       const float x = bf16_elem(vd[i], j);
       float a, da;
-      act_and_grad(act, bf16_elem(vg[i], j), a, da);
+      act_and_grad(ACT, bf16_elem(vg[i], j), a, da);
       d[0][i][j] = x * bf16_elem(vu[i], j) * da;
       d[1][i][j] = x * a;
     }
 
   if (q) {
+    // lane l16 < 8 of a DPP row: the group of half l16/4, token 4rq + l16%4
+    float amax = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float a = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(d[h][i][j]));
-        const GroupRule r = group_rule<MODE>(row16_max(a));
-        const int64_t m = m0 + i;
-        if (m < M) {
-          const float* v = d[h][i];
-          const v2u o = {pack_e4m3x4(apply<MODE>(v[0], r), apply<MODE>(v[1], r),
-                                     apply<MODE>(v[2], r), apply<MODE>(v[3], r)),
-                         pack_e4m3x4(apply<MODE>(v[4], r), apply<MODE>(v[5], r),
-                                     apply<MODE>(v[6], r), apply<MODE>(v[7], r))};
-          __builtin_nontemporal_store(o, reinterpret_cast<v2u*>(q + m * 2 * F + h * F + f0));
-          if (l16 == 0) s[(h * (F / kGroup) + fb) * M + m] = r.s;
-        }
+        for (int j = 0; j < 8; j += 2) a = max3abs(a, d[h][i][j], d[h][i][j + 1]);
+        a = row16_max(a);
+        amax = l16 == 4 * h + i ? a : amax;
       }
+    const GroupRule mine = group_rule<MODE>(amax);
+    const __amdgpu_buffer_rsrc_t rq_ = make_rsrc(q + mb * 2 * F, live * F * 2);
+    if (l16 < 8 && m0 + (l16 & 3) < M)
+      s[((l16 >> 2) * (F / kGroup) + fb) * M + m0 + (l16 & 3)] = mine.s;
+    auto each = [&](auto hi) {  // (the lane to broadcast from is an immediate)
+      constexpr int h = decltype(hi)::value / 4, i = decltype(hi)::value % 4;
+      const GroupRule r = rule_of_lane<MODE, decltype(hi)::value>(mine);
+      const float* v = d[h][i];
+      const v2u o = {pack_e4m3x4(apply<MODE>(v[0], r), apply<MODE>(v[1], r), apply<MODE>(v[2], r),
+                                 apply<MODE>(v[3], r)),
+                     pack_e4m3x4(apply<MODE>(v[4], r), apply<MODE>(v[5], r), apply<MODE>(v[6], r),
+                                 apply<MODE>(v[7], r))};
+      __builtin_amdgcn_raw_buffer_store_b64(
+          o, rq_, (uint32_t)((4 * rq + i) * 2 * fs + h * fs + (int)f0), 0, kNonTemporal);
+    };
+    each(std::integral_constant<int, 0>{});
+    each(std::integral_constant<int, 1>{});
+    each(std::integral_constant<int, 2>{});
+    each(std::integral_constant<int, 3>{});
+    each(std::integral_constant<int, 4>{});
+    each(std::integral_constant<int, 5>{});
+    each(std::integral_constant<int, 6>{});
+    each(std::integral_constant<int, 7>{});
   }
   if (!qt) return;
 
@@ -106,43 +176,54 @@ __global__ __launch_bounds__(kBwThreads) void gated_backward_kernel(
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float a = fmaxf(fmaxf(fabsf(d[h][0][j]), fabsf(d[h][1][j])),
-                      fmaxf(fabsf(d[h][2][j]), fabsf(d[h][3][j])));
+      float a = max3abs(max3abs(0.f, d[h][0][j], d[h][1][j]), d[h][2][j], d[h][3][j]);
       a = fmaxf(a, __shfl_xor(a, 16));
       a = fmaxf(a, __shfl_xor(a, 32));
-      if ((t & 63) < 16) colmax[wave][h][8 * l16 + j] = a;
+      if ((t & 63) < 16) sh.colmax[wave][h][8 * l16 + j] = a;
     }
   __syncthreads();
   if (t < 256) {
     const int h = t >> 7, c = t & 127;
     float a = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) a = fmaxf(a, colmax[w][h][c]);
+    for (int w = 0; w < 8; ++w) a = fmaxf(a, sh.colmax[w][h][c]);
     const GroupRule r = group_rule<MODE>(a);
-    colrule[h][c] = r;
+    sh.colmul[h][c] = rule_word<MODE>(r);
     st[tb * 2 * F + h * F + (int64_t)fb * kGroup + c] = r.s;
   }
   __syncthreads();
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    const v4f w0 = *reinterpret_cast<const v4f*>(&sh.colmul[h][8 * l16]);
+    const v4f w1 = *reinterpret_cast<const v4f*>(&sh.colmul[h][8 * l16 + 4]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const GroupRule r = colrule[h][8 * l16 + j];
+      const GroupRule r = word_rule<MODE>(j < 4 ? w0[j] : w1[j - 4]);
       const uint32_t w = pack_e4m3x4(apply<MODE>(d[h][0][j], r), apply<MODE>(d[h][1][j], r),
                                      apply<MODE>(d[h][2][j], r), apply<MODE>(d[h][3][j], r));
-      *reinterpret_cast<uint32_t*>(tile[h] + tile_at(8 * l16 + j, rq)) = w;
+      *reinterpret_cast<uint32_t*>(sh.tile[h] + tile_at(8 * l16 + j, rq)) = w;
     }
+  }
   __syncthreads();
   // 2 x 128 features x 8 pieces of 16 tokens, 4 per lane
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int p = t + kBwThreads * u;
     const int h = p >> 10, c = (p >> 3) & 127, piece = p & 7;
-    const v4u o = *reinterpret_cast<const v4u*>(tile[h] + tile_at(c, 4 * piece));
+    const v4u o = *reinterpret_cast<const v4u*>(sh.tile[h] + tile_at(c, 4 * piece));
     __builtin_nontemporal_store(
         o, reinterpret_cast<v4u*>(qt + (h * F + (int64_t)fb * kGroup + c) * Mp + tb * kGroup +
                                   16 * piece));
   }
+}
+
+template <int MODE, int ACT>
+__global__ __launch_bounds__(kBwThreads) void gated_backward_kernel(
+    const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu, int64_t M, int64_t F,
+    uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
+    float* __restrict__ st, int64_t Mp, int n_fblk) {
+  __shared__ __attribute__((aligned(16))) BwShared sh;
+  gated_backward<MODE, ACT>(dh, gu, M, F, q, s, qt, st, Mp, n_fblk, sh);
 }
 
 hipError_t launch_gated_backward(const void* dh, const void* gu, int64_t M, int64_t F, int act,
@@ -150,10 +231,13 @@ hipError_t launch_gated_backward(const void* dh, const void* gu, int64_t M, int6
                                  hipStream_t stream) {
   const int64_t n_fblk = F / kGroup, tb = (M + kGroup - 1) / kGroup;
   if (n_fblk * tb > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = mode == 0 ? gated_backward_kernel<0> : gated_backward_kernel<1>;
+  auto kern = act == kActSilu
+                  ? (mode == 0 ? gated_backward_kernel<0, kActSilu> : gated_backward_kernel<1, kActSilu>)
+                  : (mode == 0 ? gated_backward_kernel<0, kActGeluTanh>
+                               : gated_backward_kernel<1, kActGeluTanh>);
   hipLaunchKernelGGL(kern, dim3((unsigned)(n_fblk * tb)), dim3(kBwThreads), 0, stream,
-                     static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gu), M, F, act,
-                     q, s, qt, st, tb * kGroup, (int)n_fblk);
+                     static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gu), M, F, q,
+                     s, qt, st, tb * kGroup, (int)n_fblk);
   return hipGetLastError();
 }
 

@@ -445,6 +445,7 @@ fp8q_status fp8q_grouped_gemm_gated(const uint8_t* a_q, const float* a_s, int64_
  * Either pair may be NULL: it is then not computed.
  *   dh      : [M][F] bfloat16; gate_up : [M][2F] bfloat16 (from fp8q_gemm_gated).
  *   M >= 0, F >= 0 with F % 128 == 0.
+ * FP8Q_ERR_UNSUPPORTED: F > 2^22 (32-bit offsets within 128 tokens).
  * dY is not rounded before it is quantized; its FP32 values carry a relative
  * error of a few 2^-24, so a code can differ from that of the exact dY only
  * where the exact value lies that close to a rounding boundary.

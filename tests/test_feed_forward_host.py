@@ -147,6 +147,7 @@ def test_gated_backward_refusals(lib):
     assert f(A, A, 4, 128, 2, 0, A, A, A, A, None) == E_ENUM
     assert f(A, A, 4, 128, 0, 2, A, A, A, A, None) == E_ENUM
     assert f(None, None, 0, 128, 0, 0, None, None, None, None, None) == OK
+    assert f(A, A, 4, (1 << 22) + 128, 0, 0, A, A, A, A, None) == E_UNSUP
 
 
 # ------------------------------------------------------------------ the binding
