@@ -14,7 +14,10 @@ library then validates sizes, alignment and enums itself.
 
 Allocation helpers (``quantize_act``, ``quantize_weight``, ``gemm``,
 ``grouped_gemm``, ...) allocate outputs with torch on the input's device and
-then call the entry points.
+then call the entry points.  Those of the feed-forward operators
+(``quantize_token_i8``, ``gemm_i8``, ``gemm_gated``, ...) do so in compiled code
+(csrc/calls.cpp) when every argument is as it should be and no stream is named;
+else they take the Python path, whose checks say what is wrong.
 """
 
 import ctypes
@@ -28,6 +31,9 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"libfp8q.so not found at {LIB_PATH}; build it with "
         "`python fine_grained_block_fp8q_amd/build.py` (hipcc, gfx950)")
+
+if not os.path.exists(os.path.join(_PKG, "_calls.so")):
+    raise ImportError(f"_calls.so not found in {_PKG}; build it as libfp8q.so")
 
 lib = ctypes.CDLL(LIB_PATH)
 
@@ -432,14 +438,9 @@ def fp8q_quantize_token_i8(x, q, s, stream=None):
     import torch
     wh = "fp8q_quantize_token_i8"
     M, K = _dims(wh, x, 2, "x")
-    _need(wh, x.device, ("q", q, torch.int8, (M, -(-K // 16) * 16)), ("s", s, torch.float32, (M,)))
-    _quantize_token_i8(wh, x, M, K, q, s, stream)
-
-
-def _quantize_token_i8(wh, x, M, K, q, s, stream):
-    import torch
     dev = x.device
-    _need(wh, dev, ("x", x, torch.bfloat16, (M, K)))
+    _need(wh, dev, ("x", x, torch.bfloat16, (M, K)), ("q", q, torch.int8, (M, -(-K // 16) * 16)),
+          ("s", s, torch.float32, (M,)))
     _invoke(lib.fp8q_quantize_token_i8, (x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(),
                                          _stream(stream, dev)), wh)
 
@@ -465,13 +466,8 @@ def fp8q_gemm_i8(a_q, a_s, w_q, w_s, c, bias=None, stream=None):
     """c[M][N] (float32 or bfloat16) = (int8 a_q[M][K] x w_q[N][K]^T) * a_s[M]
     * w_s[N] (+ bias[N])."""
     wh = "fp8q_gemm_i8"
-    M, N = _rows(wh, a_q, w_q)
-    _req(wh, "c", c, ["f32", "bf16"], (M, N), a_q.device)
-    _gemm_i8(wh, a_q, a_s, w_q, w_s, c, bias, stream)
-
-
-def _gemm_i8(wh, a_q, a_s, w_q, w_s, c, bias, stream):
     M, N, K, dev = _i8_args(wh, a_q, a_s, w_q, w_s)
+    _req(wh, "c", c, ["f32", "bf16"], (M, N), dev)
     if bias is not None:
         _req(wh, "bias", bias, ["f32"], (N,), dev)
     _invoke(lib.fp8q_gemm_i8, (a_q.data_ptr(), a_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(),
@@ -489,14 +485,9 @@ def fp8q_gemm_i8_gated(a_q, a_s, w_q, w_s, h, act="silu", stream=None):
     """h[M][F] = act(Y[:, :F]) * Y[:, F:], Y the int8 product of a_q[M][K] with
     the stacked gate and up weights w_q[2F][K], scaled by a_s[M] and w_s[2F]."""
     wh = "fp8q_gemm_i8_gated"
-    M, N = _rows(wh, a_q, w_q)
-    _req(wh, "h", h, ["f32", "bf16"], (M, N // 2), a_q.device)
-    _gemm_i8_gated(wh, a_q, a_s, w_q, w_s, h, act, stream)
-
-
-def _gemm_i8_gated(wh, a_q, a_s, w_q, w_s, h, act, stream):
     M, N, K, dev = _i8_args(wh, a_q, a_s, w_q, w_s)
     _gate_rows(wh, N, 1)
+    _req(wh, "h", h, ["f32", "bf16"], (M, N // 2), dev)
     _invoke(lib.fp8q_gemm_i8_gated, (a_q.data_ptr(), a_s.data_ptr(), w_q.data_ptr(),
                                      w_s.data_ptr(), M, N // 2, K, _act(wh, act), h.data_ptr(),
                                      _out_code(wh, h), _stream(stream, dev)), wh)
@@ -656,64 +647,122 @@ def grouped_gemm(a_q, a_s, off, w_q, w_s, out_dtype=None, stream=None, precise=F
     return c
 
 
+_native = None
+
+
+def _compiled():
+    """The module of csrc/calls.cpp with this library's entry points, and the
+    output codes of the dtypes it allocates."""
+    global _native, _OUT_OF
+    import torch       # its libraries first
+    from . import _calls
+    _calls.entries(*(ctypes.cast(getattr(lib, "fp8q_" + n), _p).value for n in
+                     ("quantize_token_i8", "gemm_i8", "gemm_i8_gated", "gemm_gated",
+                      "grouped_gemm_gated", "gated_backward")))
+    _OUT_OF = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+    _native = _calls
+    return _calls
+
+
+def _refused(status, where):
+    raise Fp8qError(status, where)
+
+
 def quantize_token_i8(x, stream=None):
     """x: bf16 [M][K] -> (int8 codes [M][Kp], float32 scales [M]); Kp is K up to
     a multiple of 16, with zero codes past K."""
-    import torch
     wh = "fp8q_quantize_token_i8"
+    if stream is None:
+        r = (_native or _compiled()).quantize_token_i8(x)
+        if r is not None:
+            return r if type(r) is not int else _refused(r, wh)
+    import torch
     M, K = _dims(wh, x, 2, "x")
     q = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=x.device)
     s = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _quantize_token_i8(wh, x, M, K, q, s, stream)
+    fp8q_quantize_token_i8(x, q, s, stream)
     return q, s
 
 
 def gemm_i8(a_q, a_s, w_q, w_s, bias=None, out_dtype=None, stream=None):
-    import torch
     wh = "fp8q_gemm_i8"
-    c = torch.empty(_rows(wh, a_q, w_q), dtype=out_dtype or torch.float32, device=a_q.device)
-    _gemm_i8(wh, a_q, a_s, w_q, w_s, c, bias, stream)
+    if stream is None:
+        native = _native or _compiled()
+        out = OUT_F32 if out_dtype is None else _OUT_OF.get(out_dtype)
+        if out is not None:
+            r = native.gemm_i8(a_q, a_s, w_q, w_s, bias, out)
+            if r is not None:
+                return r if type(r) is not int else _refused(r, wh)
+    import torch
+    M, N = _rows(wh, a_q, w_q)
+    c = torch.empty((M, N), dtype=out_dtype or torch.float32, device=a_q.device)
+    fp8q_gemm_i8(a_q, a_s, w_q, w_s, c, bias, stream)
     return c
 
 
 def gemm_i8_gated(a_q, a_s, w_q, w_s, act="silu", out_dtype=None, stream=None):
     """h = act(gate) * up (bfloat16 unless out_dtype says float32)."""
-    import torch
     wh = "fp8q_gemm_i8_gated"
+    if stream is None:
+        native = _native or _compiled()
+        out = OUT_BF16 if out_dtype is None else _OUT_OF.get(out_dtype)
+        if out is not None:
+            r = native.gemm_i8_gated(a_q, a_s, w_q, w_s, _act(wh, act), out)
+            if r is not None:
+                return r if type(r) is not int else _refused(r, wh)
+    import torch
     M, N = _rows(wh, a_q, w_q)
     h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
-    _gemm_i8_gated(wh, a_q, a_s, w_q, w_s, h, act, stream)
+    fp8q_gemm_i8_gated(a_q, a_s, w_q, w_s, h, act, stream)
     return h
+
+
+def _gated(wh, a_q, a_s, off, w_q, w_s, act, out_dtype, save_gate_up, stream):
+    if stream is None:
+        native = _native or _compiled()
+        out = OUT_BF16 if out_dtype is None else _OUT_OF.get(out_dtype)
+        if out is not None:
+            r = native.gemm_gated(a_q, a_s, off, w_q, w_s, _act(wh, act), out, save_gate_up)
+            if r is not None:
+                return r if type(r) is not int else _refused(r, wh)
+    import torch
+    M = _dims(wh, a_q, 2, "a_q")[0]
+    N = _dims(wh, w_q, 2 if off is None else 3, "w_q")[-2]
+    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
+    gu = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device) if save_gate_up else None
+    if off is None:
+        fp8q_gemm_gated(a_q, a_s, w_q, w_s, h, act, gu, stream)
+    else:
+        fp8q_grouped_gemm_gated(a_q, a_s, off, w_q, w_s, h, act, gu, stream)
+    return (h, gu) if save_gate_up else h
 
 
 def gemm_gated(a_q, a_s, w_q, w_s, act="silu", out_dtype=None, save_gate_up=False, stream=None):
     """h = act(gate) * up (bfloat16 unless out_dtype says float32); with
     save_gate_up, (h, the bfloat16 [gate | up] the backward pass takes)."""
-    import torch
-    M, N = a_q.shape[0], w_q.shape[0]
-    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
-    gu = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device) if save_gate_up else None
-    fp8q_gemm_gated(a_q, a_s, w_q, w_s, h, act, gu, stream)
-    return (h, gu) if save_gate_up else h
+    return _gated("fp8q_gemm_gated", a_q, a_s, None, w_q, w_s, act, out_dtype, save_gate_up, stream)
 
 
 def grouped_gemm_gated(a_q, a_s, off, w_q, w_s, act="silu", out_dtype=None, save_gate_up=False,
                        stream=None):
     """gemm_gated by expert; rows at or past off[G] are not written."""
-    import torch
-    M, N = a_q.shape[0], w_q.shape[1]
-    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
-    gu = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device) if save_gate_up else None
-    fp8q_grouped_gemm_gated(a_q, a_s, off, w_q, w_s, h, act, gu, stream)
-    return (h, gu) if save_gate_up else h
+    wh = "fp8q_grouped_gemm_gated"
+    _dims(wh, off, 1, "off")
+    return _gated(wh, a_q, a_s, off, w_q, w_s, act, out_dtype, save_gate_up, stream)
 
 
 def gated_backward(dh, gate_up, act="silu", mode="f32", rows=True, tokens=True, stream=None):
     """(q, s, qt, st): dY in E4M3 along the features and along the tokens, for
     gemm (dX = dY W) and gemm_rowscaled (dW = dY^T X).  rows=False or
     tokens=False leaves that pair out (None)."""
+    wh = "fp8q_gated_backward"
+    if stream is None:
+        r = (_native or _compiled()).gated_backward(dh, gate_up, _act(wh, act), _MODES[mode], rows,
+                                                    tokens)
+        if r is not None:
+            return r if type(r) is not int else _refused(r, wh)
     import torch
-    M, F = dh.shape
+    M, F = _dims(wh, dh, 2, "dh")
     dev, groups = dh.device, -(-M // GROUP)
     q = s = qt = st = None
     if rows:

@@ -21,6 +21,9 @@ LIB_DEBUG = os.path.join(PKG, "libfp8q_debug.so")
 # Measurement support for bench.py --copy-probe (streaming-bandwidth ceiling
 # and counter calibration); not part of the method's C ABI.
 LIB_PROBE = os.path.join(PKG, "libfp8q_probe.so")
+# The compiled calls of the Python package (a CPython module against torch's
+# headers; it gets the entry points' addresses from the package).
+LIB_CALLS = os.path.join(PKG, "_calls.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -82,13 +85,31 @@ def build(verbose=False):
     FP8Q_DEBUG_CHECKS variant libfp8q_debug.so (always rebuilds)."""
     from concurrent.futures import ThreadPoolExecutor
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(3) as ex:
+    with ThreadPoolExecutor(4) as ex:
         jobs = [ex.submit(_build_one, LIB, "", [], verbose),
                 ex.submit(_build_one, LIB_DEBUG, "_debug", ["-DFP8Q_DEBUG_CHECKS"], verbose),
-                ex.submit(_build_probe, verbose)]
+                ex.submit(_build_probe, verbose), ex.submit(_build_calls, verbose)]
         for j in jobs:
             j.result()
     return LIB
+
+
+def _build_calls(verbose):
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    tmp = LIB_CALLS + ".tmp"
+    out = _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE,
+                "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+                "-isystem", os.path.join(rocm, "include"), os.path.join(CSRC, "calls.cpp"),
+                "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                "-lc10_hip", "-o", tmp])
+    if verbose and out.strip():
+        print(out)
+    os.replace(tmp, LIB_CALLS)
 
 
 def _build_probe(verbose):

@@ -210,3 +210,28 @@ def test_binding_refusals_backward(no_stream):
               dict(q=None, s=None, qt=None, st=None), dict(qt=_t((2 * F, M), u8)),
               dict(st=_t((2, 2 * F), f32)), dict(s=_t((M, 2), f32)), dict(act="relu"),
               dict(dh=_t((M, 100), bf16), gate_up=_t((M, 200), bf16))])
+
+
+def test_allocating_calls_refuse_as_the_wrappers_do(no_stream):
+    """Arguments the compiled path does not take reach the wrappers' checks."""
+    a, s, w, ws = _t((4, 64), i8), _t((4,), f32), _t((10, 64), i8), _t((10,), f32)
+    for args, kw in (((a, s, _t((10, 80), i8), ws), {}), ((a, s[:2], w, ws), {}),
+                     ((a, s, w, ws), dict(out_dtype=torch.float16)),
+                     ((a, s, w, ws), dict(bias=_t((9,), f32))), ((None, s, w, ws), {})):
+        with pytest.raises(ValueError):
+            fq.gemm_i8(*args, **kw)
+    with pytest.raises(ValueError):
+        fq.gemm_i8_gated(a, s, w[:9], ws[:9])
+    with pytest.raises(ValueError):
+        fq.gemm_i8_gated(a, s, w, ws, act="relu")
+    with pytest.raises(ValueError):
+        fq.quantize_token_i8(_t((4, 64), f32))
+    with pytest.raises(ValueError):
+        fq.gemm_gated(_t((4, 128), u8), _t((1, 4), f32), _t((128, 128), u8), _t((1, 1), f32))
+    with pytest.raises(ValueError):
+        fq.grouped_gemm_gated(_t((4, 128), u8), _t((1, 4), f32), None, _t((2, 256, 128), u8),
+                              _t((2, 2, 1), f32))
+    with pytest.raises(ValueError):
+        fq.gated_backward(_t((4, 128), bf16), _t((4, 256), bf16), rows=False, tokens=False)
+    with pytest.raises(ValueError):
+        fq.gated_backward(_t((4, 128), bf16), _t((4, 128), bf16))
