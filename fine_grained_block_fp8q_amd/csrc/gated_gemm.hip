@@ -104,9 +104,9 @@ hipError_t launch_gated_few(const uint8_t* a_q, const float* a_s, int64_t M, con
 //   64 x 128                  24.5  24.4  24.5  27.6  44    83    157
 //   128 x 128                 43    46    46    46    48.5  65    126
 //   256 x 256                       58    79    79    79.5  82    104
-constexpr TileVariant kGatedVariants[] = {{64, 64, 128, 371, 430, 721, 600},
-                                          {128, 128, 128, 730, 777, 1071, 1500},
-                                          {256, 256, 256, 1275, 1707, 3414, 5000}};
+constexpr TileVariant kGatedVariants[] = {{64, 64, 128, 371, 430, 721, 1200},
+                                          {128, 128, 128, 730, 777, 1071, 2200},
+                                          {256, 256, 256, 1275, 1707, 3414, 6000}};
 
 // off NULL: one dense block of weights; else G experts.
 hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, const int32_t* off,

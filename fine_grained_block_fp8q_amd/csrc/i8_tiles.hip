@@ -403,9 +403,9 @@ hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q,
 //   64 x 128      19.6  19.7  20.1  22.6  39    76
 //   128 x 128     23.6  24.7  24.9  25.8  33    57    108
 //   256 x 256           68    68    69    69    72    90
-constexpr TileVariant kI8Variants[] = {{64, 64, 128, 273, 325, 625, 800},
-                                       {128, 128, 128, 350, 496, 932, 1600},
-                                       {256, 256, 256, 1027, 1375, 2750, 7000}};
+constexpr TileVariant kI8Variants[] = {{64, 64, 128, 273, 325, 625, 1400},
+                                       {128, 128, 128, 350, 496, 932, 2400},
+                                       {256, 256, 256, 1027, 1375, 2750, 8000}};
 
 static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                             const float* w_s, const float* bias, int64_t M, int64_t N, int64_t K,
