@@ -414,3 +414,21 @@ def test_training_step_gradients(M):
     dY = off.gated_backward("silu", _value(dh), Y)
     for got, ref in ((_value(dx), dY @ _value(w)), (_value(dw), dY.T @ _value(x))):
         assert np.linalg.norm(got - ref) <= 0.1 * np.linalg.norm(ref)
+
+
+def test_example_trains_and_serves(capsys):
+    """examples/feed_forward.py at a small size: the loss falls, INT8 serving
+    stays near the FP8 layer, the grouped call near each expert's own."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward_example", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses = ex.main(["--tokens", "512", "--hidden", "256", "--ffn", "256", "--steps", "12",
+                      "--lr", "100"])
+    assert losses[-1] < 0.9 * losses[0]
+    out = capsys.readouterr().out
+    assert float(out.split("served in INT8: ")[1].split()[0]) < 0.1
+    assert float(out.split("within ")[1].split()[0]) < 1e-2
