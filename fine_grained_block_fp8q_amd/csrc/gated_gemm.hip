@@ -104,9 +104,10 @@ hipError_t launch_gated_few(const uint8_t* a_q, const float* a_s, int64_t M, con
 //   64 x 128                  24.5  24.4  24.5  27.6  44    83    157
 //   128 x 128                 43    46    46    46    48.5  65    126
 //   256 x 256                       58    79    79    79.5  82    104
-constexpr TileVariant kGatedVariants[] = {{64, 64, 128, 371, 430, 721, 1200},
-                                          {128, 128, 128, 730, 777, 1071, 2200},
-                                          {256, 256, 256, 1275, 1707, 3414, 6000}};
+constexpr TileVariant kGatedVariants[] = {{64, 64, 128, 3380, 350, 388, 619, 1210, 1.0},
+                                          {128, 128, 128, 3350, 596, 763, 948, 1430, 1.0},
+                                          {256, 256, 256, 0, 1280, 1480, 2958, 7800, 1.0}};
+constexpr FewRowsCost kGatedFew = {3380, 1.28, 1.59, 18.3, 1.0};
 
 // off NULL: one dense block of weights; else G experts.
 hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, const int32_t* off,
@@ -119,7 +120,7 @@ hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, co
   if (off)
     return launch_grouped_gated_tiles(a_q, a_s, M, off, G, w_q, w_s, F, K, act, h, out_bf16, gu,
                                       cus, stream);
-  const int tile = pick_variant(kGatedVariants, M, 2 * F, K / 128, cus);
+  const int tile = pick_variant(kGatedVariants, kGatedFew, M, 2 * F, K, 128, cus);
   if (tile == 0)
     return launch_gated_few(a_q, a_s, M, w_q, w_s, F, K, act, h, out_bf16, gu, stream);
   return launch_gated_tiles(a_q, a_s, M, w_q, w_s, F, K, act, h, out_bf16, gu, tile, stream);

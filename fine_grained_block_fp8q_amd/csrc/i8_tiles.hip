@@ -17,9 +17,14 @@
 // chunk g is multiplied, the second half of its W fragments is read; while
 // step 1 is, all of A's fragments of chunk g + 1 and the first half of W's.  So
 // A's unit is free one step before W's, and with two units of A and three of W
-// (160 KB) their refills go out in alternate steps, 8 loads a wave beside 64
-// products, two steps (A) and three (W) before they are needed.  One barrier a
-// step, a few products before its end.
+// (160 KB in the largest tile) their refills go out in alternate steps, 8 loads
+// a wave beside 64 products, two steps (A) and three (W) before they are needed.
+// One barrier a step, a few products before its end.
+//
+// 4096 x 4096 x 7168: 86 to 90 us, 2650 to 2790 TOP/s.  Without the LDS reads it
+// takes 83, without the loads 77, without both 72; the chip is held back by its
+// power (1.95 to 2.1 GHz): 512 rows, an eighth of the CUs, take 67 where these
+// do and 59 without.
 //
 // The product is formed transposed (weight rows are the instruction's rows), so
 // a lane holds 4 consecutive outputs of one activation row; the epilogue
@@ -38,12 +43,12 @@ namespace fp8q {
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool GATED_, bool BF16_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int NA_, bool GATED_, bool BF16_>
 struct I8Cfg {
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr bool GATED = GATED_, BF16 = BF16_;
   static constexpr int BK = 128;                      // bytes of K a unit
-  static constexpr int NA = 2, NW = 3;                // units of A and of W
+  static constexpr int NA = NA_, NW = NA + 1;         // units of A and of W
   static constexpr int NWAVES = WAVES_M * WAVES_N, THREADS = NWAVES * 64;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int MB = WM / 16, NB = WN / 16;
@@ -136,10 +141,10 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
   static_assert(Cfg::WNO % RL == 0, "a load of the workgroup is all gate or all up rows");
   const uint32_t voff = (uint32_t)((wave * 8 + pr) * (int)K + kc);
   const int k_lim = (int)K - kc, ks = (int)K;
-  auto load_a = [&](int g, int d) {
+  auto load_a = [&](int g, int unit, int d) {
     const uint32_t v = g * Cfg::BK < k_lim ? voff : kOutOfRange;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        ra, to_lds(smem + (g % Cfg::NA) * Cfg::A_UNIT + (d * Cfg::NWAVES + wave) * 1024), 16, v,
+        ra, to_lds(smem + unit * Cfg::A_UNIT + (d * Cfg::NWAVES + wave) * 1024), 16, v,
         g * Cfg::BK + d * RL * ks, 0, 0);
   };
   auto load_w = [&](int g, int unit, int d) {
@@ -173,17 +178,16 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
   // Chunks go in pairs (A has two units); past K they are zeros.
   const int chunks = (int)((K + 2 * Cfg::BK - 1) / (2 * Cfg::BK)) * 2;
 
-  // In the order of the steady state: A and W of chunk 0, W of 1, A of 1, W of 2.
-#pragma unroll
-  for (int d = 0; d < LA; ++d) load_a(0, d);
+  // In the order of the steady state: W of chunk 0, A of 0, W of 1, A of 1, ...
 #pragma unroll
   for (int d = 0; d < LW; ++d) load_w(0, 0, d);
 #pragma unroll
-  for (int d = 0; d < LW; ++d) load_w(1, 1, d);
+  for (int x = 0; x < Cfg::NA; ++x) {
 #pragma unroll
-  for (int d = 0; d < LA; ++d) load_a(1, d);
+    for (int d = 0; d < LA; ++d) load_a(x, x, d);
 #pragma unroll
-  for (int d = 0; d < LW; ++d) load_w(2, 2, d);
+    for (int d = 0; d < LW; ++d) load_w(x + 1, x + 1, d);
+  }
 
   // The scheduling barriers fix the order product by product: the compiler
   // left to itself reads fragments right before their products, and loads sent
@@ -192,9 +196,10 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
   // waves meet.
   constexpr int T = MB * NB, kLead = T >= 16 ? 4 : 0, kSpan = T - 2 * kLead;
   v4i a0[MB], a1[2][MB], w0[NB], w1[NB];
-  // Step 0 of chunk g (W unit u): beside its products, the reads of w1 and the
-  // loads of A of chunk g + 2, whose unit all waves have read.
-  auto step0 = [&](int g, int u) {
+  // Step 0 of chunk g (units t of A and u of W): beside its products, the reads
+  // of w1 and the loads of A of chunk g + NA into unit t, which all waves have
+  // read.
+  auto step0 = [&](int g, int t, int u) {
 #pragma unroll
     for (int k = 0; k < T; ++k) {
       mfma_i8(acc[k / NB][k % NB], w0[k % NB], a0[k / NB]);
@@ -203,19 +208,19 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
         if (j * kSpan / NB == k) read_w(w1[j], u, 1, j);
 #pragma unroll
       for (int d = 0; d < LA; ++d)
-        if ((2 * d + 1) * kSpan / (2 * LA) == k) load_a(g + 2, d);
+        if ((2 * d + 1) * kSpan / (2 * LA) == k) load_a(g + Cfg::NA, t, d);
       if (k == T - 1 - kLead) {
         // W's unit u is read; A and W of chunk g + 1 have landed (what was
-        // issued after them: W of g + 2, A of g + 2)
-        wait_vmcnt<LA + LW>();
+        // issued after them: W and A of chunks g + 2 to g + NA)
+        wait_vmcnt<(Cfg::NA - 1) * (LA + LW)>();
         lds_barrier();
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   // Step 1: the reads of A (both halves) and the first half of W of chunk
-  // g + 1, and the loads of W of chunk g + 3 into unit u.
-  auto step1 = [&](int g, const v4i (&x)[MB], v4i (&y)[MB], int u, int u1) {
+  // g + 1 (units t1 and u1), and the loads of W of chunk g + NW into unit u.
+  auto step1 = [&](int g, const v4i (&x)[MB], v4i (&y)[MB], int t1, int u, int u1) {
     constexpr int R = 2 * MB + NB;
 #pragma unroll
     for (int k = 0; k < T; ++k) {
@@ -224,22 +229,22 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
       for (int r = 0; r < R; ++r)
         if (r * kSpan / R == k) {
           if (r == 0)
-            read_a(a0[0], (g + 1) & 1, 0, 0);
+            read_a(a0[0], t1, 0, 0);
           else if (r <= NB)
             read_w(w0[r - 1], u1, 0, r - 1);
           else if (r < NB + MB)
-            read_a(a0[r - NB], (g + 1) & 1, 0, r - NB);
+            read_a(a0[r - NB], t1, 0, r - NB);
           else
-            read_a(y[r - NB - MB], (g + 1) & 1, 1, r - NB - MB);
+            read_a(y[r - NB - MB], t1, 1, r - NB - MB);
         }
 #pragma unroll
       for (int d = 0; d < LW; ++d)
-        if ((2 * d + 1) * kSpan / (2 * LW) == k) load_w(g + 3, u, d);
+        if ((2 * d + 1) * kSpan / (2 * LW) == k) load_w(g + Cfg::NW, u, d);
       if (k == T - 1 - kLead) lds_barrier();  // A's unit of chunk g + 1 is read
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  wait_vmcnt<LA + 2 * LW>();
+  wait_vmcnt<(Cfg::NA - 1) * LA + Cfg::NA * LW>();
   lds_barrier();
 #pragma unroll
   for (int i = 0; i < MB; ++i) read_a(a0[i], 0, 0, i);
@@ -248,13 +253,15 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
 #pragma unroll
   for (int j = 0; j < NB; ++j) read_w(w0[j], 0, 0, j);
   lds_barrier();  // A's unit of chunk 0 is read
-  int u = 0;
+  int t = 0, u = 0;
   for (int g = 0; g < chunks; g += 2) {
+    const int t1 = t + 1 == Cfg::NA ? 0 : t + 1, t2 = t1 + 1 == Cfg::NA ? 0 : t1 + 1;
     const int u1 = u + 1 == Cfg::NW ? 0 : u + 1, u2 = u1 + 1 == Cfg::NW ? 0 : u1 + 1;
-    step0(g, u);
-    step1(g, a1[0], a1[1], u, u1);
-    step0(g + 1, u1);
-    step1(g + 1, a1[1], a1[0], u1, u2);
+    step0(g, t, u);
+    step1(g, a1[0], a1[1], t1, u, u1);
+    step0(g + 1, t1, u1);
+    step1(g + 1, a1[1], a1[0], t2, u1, u2);
+    t = t2;
     u = u2;
   }
   // The rows' and columns' scales and the bias, for the epilogue.  (Asked for
@@ -367,9 +374,10 @@ static hipError_t launch_tiles(I8Args p, hipStream_t stream) {
 
 template <bool GATED, bool BF16>
 static hipError_t launch_tile(const I8Args& p, int tile, hipStream_t stream) {
-  return tile == 256   ? launch_tiles<I8Cfg<256, 256, 2, 2, GATED, BF16>>(p, stream)
-         : tile == 128 ? launch_tiles<I8Cfg<128, 128, 2, 2, GATED, BF16>>(p, stream)
-                       : launch_tiles<I8Cfg<64, 128, 2, 2, GATED, BF16>>(p, stream);
+  return tile == 256   ? launch_tiles<I8Cfg<256, 256, 2, 2, 2, GATED, BF16>>(p, stream)
+         : tile == 128 ? launch_tiles<I8Cfg<128, 128, 2, 2, 2, GATED, BF16>>(p, stream)
+         : tile == 64  ? launch_tiles<I8Cfg<64, 64, 2, 1, 3, GATED, BF16>>(p, stream)
+                       : launch_tiles<I8Cfg<32, 64, 1, 2, 3, GATED, BF16>>(p, stream);
 }
 
 hipError_t launch_i8_tiles(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
@@ -398,14 +406,20 @@ hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                          void* c, int out_bf16, hipStream_t stream);
 
 // Kernel times with 4096 weight rows, K = 7168, in us, by number of rows:
-//   rows          64    128   256   512   1024  2048  4096
-//   few rows      10.2  15.8  29
-//   64 x 128      19.6  19.7  20.1  22.6  39    76
-//   128 x 128     23.6  24.7  24.9  25.8  33    57    108
-//   256 x 256           68    68    69    69    72    90
-constexpr TileVariant kI8Variants[] = {{64, 64, 128, 273, 325, 625, 1400},
-                                       {128, 128, 128, 350, 496, 932, 2400},
-                                       {256, 256, 256, 1027, 1375, 2750, 8000}};
+//   rows          64    128   256   384   512   768   1024  2048  4096
+//   few rows      10.2  15.7  29
+//   32 x 64       14.2  14.3  18.3  31
+//   64 x 64       17.0  17.1  17.5  21.6  21.5  39    43
+//   128 x 128     23.6  24.7  24.7  24.9  25.2  26.1  28.6  52    108
+//   256 x 256           68    68    68    69    69    69    70    86-90
+// (64 x 128 tiles take 18.6 to 20.5 us up to 512 rows: with them beside the four
+// kept, 0.3% less time over 160 random shapes.)  The two smallest have rings of
+// three chunks of A and four of W and share a CU.
+constexpr TileVariant kI8Variants[] = {{32, 32, 64, 2680, 182, 189, 255, 640, 1.13},
+                                       {64, 64, 64, 2490, 229, 249, 299, 1260, 1.17},
+                                       {128, 128, 128, 2770, 320, 426, 758, 2350, 1.23},
+                                       {256, 256, 256, 4840, 1012, 1129, 2372, 8300, 1.09}};
+constexpr FewRowsCost kI8Few = {3130, 1.17, 1.74, 11.4, 1.1};
 
 static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                             const float* w_s, const float* bias, int64_t M, int64_t N, int64_t K,
@@ -414,7 +428,7 @@ static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
     return hipGetLastError();
-  const int tile = pick_variant(kI8Variants, M, gated ? 2 * N : N, (K + 127) / 128, cus);
+  const int tile = pick_variant(kI8Variants, kI8Few, M, gated ? 2 * N : N, K, 256, cus);
   if (tile == 0)
     return launch_i8_few(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, stream);
   return launch_i8_tiles(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, tile, stream);

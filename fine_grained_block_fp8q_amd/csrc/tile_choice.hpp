@@ -5,42 +5,52 @@
 
 namespace fp8q {
 
-// A tiled kernel's costs in ns: for each 128 k with under half of the CUs at
-// work, with one workgroup on each CU and with two on each (they overlap where
-// two fit, else they follow each other), and for a tile's end.
+// A tiled kernel's times in ns, its launch and the ring's first fill included
+// in `start`: for each 128 k with up to half of the CUs at work, with one
+// workgroup on each CU and with two (they overlap where two fit, else they
+// follow each other), and for a tile's end.  `split` is the factor on the k
+// part where K is no multiple of 128: a row's 128 bytes then lie in two lines.
 struct TileVariant {
   int tile;    // what the launch is told
   int bm, bn;  // rows of activations and of weights
-  double idle, one, two, end;
+  double start, idle, one, two, end, split;
 };
 
-// The variant that takes least for M x weight_rows x 128 chunks, or 0 where the
-// kernel for few rows does: that one reads (16 + rows) * 128 bytes a chunk for
-// 16 weight rows, at 80 bytes a ns and CU, and a workgroup of it holds up to
-// 128 rows.  Besides, what one workgroup waits for before its first product and
-// after its last: 0.5 us where few rows are served, 1.8 for a tile's ring to
-// fill, and about 4 us (2 at 64 rows, where two share a CU) for each further
-// round of few-row workgroups.
-// Estimate and measurement of int8 products, us (3.5 of it the launch):
-//   120 x 897 x 592     few rows 5.2 / 5.4    64-row tiles 8.1 / 7.2
-//   911 x 1333 x 176    few rows 13.4 / 12.7  64-row tiles 7.4 / 6.6
-//   74 x 1393 x 4736    few rows 12.5 / 10.7  64-row tiles 16.8 / 16.5
-//   1679 x 5586 x 656   64-row tiles 21.7 / 25.5  128-row tiles 20.2 / 25.3
+// The kernel for few rows: a workgroup of it holds 16 weight rows and 64 or 128
+// activation rows and its 8 waves take a chunk each.  In ns, for each of those
+// activation rows: a chunk with up to half of the CUs at work and with all, and
+// each further round of workgroups.
+struct FewRowsCost {
+  double start, idle, one, round, split;
+};
+
+// The variant that takes least for M x weight_rows x K, or 0 where the kernel
+// for few rows does; the tiles take K in steps of `step`.  The constants are
+// fitted to measured times of every kernel at random shapes (M 33 to 5800,
+// weight rows 64 to 8192, K 128 to 9000).  Against the best kernel of each
+// shape the choice costs 1.1% on average and 16% at most over 156 int8 shapes,
+// 0.2% and 12% over 138 E4M3 ones.
 template <int N>
-inline int pick_variant(const TileVariant (&variants)[N], int64_t M, int64_t weight_rows,
-                        int64_t chunks, int cus) {
+inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few, int64_t M,
+                        int64_t weight_rows, int64_t K, int step, int cus) {
   auto blocks = [](int64_t x, int64_t b) { return (x + b - 1) / b; };
   if (M <= 32) return 0;
-  const int64_t few = M <= 64 ? 64 : 128;
-  const int64_t rounds = blocks(blocks(M, few) * blocks(weight_rows, 16), cus);
-  double least = (double)(rounds * chunks) * (16 + few) * 1.6 + 500.0 +
-                 (double)(rounds - 1) * (few == 64 ? 2000.0 : 4000.0);
+  const bool whole = K % 128 == 0;
+  const int64_t rows = M <= 64 ? 64 : 128;
+  const int64_t n_few = blocks(M, rows) * blocks(weight_rows, 16);
+  const int64_t rounds = blocks(n_few, cus);
+  const bool idle = 2 * (n_few - (rounds - 1) * cus) <= cus;
+  const double few_k = (double)(blocks(K, 1024) * 8) * (whole ? 1.0 : few.split);
+  double least =
+      few.start + (double)rows * (few_k * ((double)(rounds - 1) * few.one + (idle ? few.idle : few.one)) +
+                                  (double)(rounds - 1) * few.round);
+  const double chunks = (double)(blocks(K, step) * step) / 128.0;
   int best = 0;
   for (const TileVariant& v : variants) {
     const int64_t n = blocks(M, v.bm) * blocks(weight_rows, v.bn);
     const int64_t pairs = n / (2 * cus), rest = n % (2 * cus);
     const double last = rest == 0 ? 0 : rest > cus ? v.two : 2 * rest > cus ? v.one : v.idle;
-    const double t = 1800.0 + (double)chunks * ((double)pairs * v.two + last) +
+    const double t = v.start + chunks * (whole ? 1.0 : v.split) * ((double)pairs * v.two + last) +
                      (double)(2 * pairs + (rest > cus ? 2 : rest > 0 ? 1 : 0)) * v.end;
     if (t < least) {
       least = t;

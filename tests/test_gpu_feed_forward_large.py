@@ -83,6 +83,23 @@ def test_gemm_i8_gated_tiles(M, F, K, act):
         assert _close(fq().gemm_i8_gated(a, sa, w, sw, act=act, out_dtype=out), ref, rel)
 
 
+# the tiles of 32 and 64 rows: one row in the last tile, one column, one chunk of
+# K and part of it, chunks that end inside the ring's first round
+@pytest.mark.parametrize("M,N,K,bias", [(33, 70, 16, True), (65, 300, 1040, False),
+                                        (333, 1100, 1040, True), (500, 2051, 336, False),
+                                        (449, 2001, 400, True), (129, 513, 2064, False)])
+def test_gemm_i8_small_tiles(M, N, K, bias):
+    for out in (torch.bfloat16, torch.float32):
+        test_gemm_i8_tiles(M, N, K, bias, out)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,F,K", [(33, 35, 144), (97, 150, 1040), (450, 1000, 336),
+                                   (513, 1025, 528)])
+def test_gemm_i8_gated_small_tiles(M, F, K, act):
+    test_gemm_i8_gated_tiles(M, F, K, act)
+
+
 def _codes(g, *shape):
     """E4M3 codes of finite values."""
     return torch.randint(0, 127, shape, generator=g, device=DEV, dtype=torch.uint8) \
