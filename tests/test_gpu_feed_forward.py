@@ -305,6 +305,26 @@ def test_gated_backward(M, F, act, mode):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("mode", ["f32", "pow2"])
+@pytest.mark.parametrize("M,part", [(1200, 128), (1200, 384), (1150, 1100)])
+def test_gated_backward_of_a_part_is_the_part_of_it(M, part, act, mode):
+    """Few and many groups (kernels of their own) agree bit for bit: a call on
+    the first tokens gives the first rows and groups of the whole one."""
+    F = 2048
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M + part)
+    dh = torch.randn(M, F, generator=g, device=DEV).to(torch.bfloat16)
+    Y = (2 * torch.randn(M, 2 * F, generator=g, device=DEV)).to(torch.bfloat16)
+    q, s, qt, st = fq().gated_backward(dh, Y, act=act, mode=mode)
+    for n in range(0, part, part if part < 1000 else 128):
+        m = min(n + (part if part < 1000 else 128), M)
+        q1, s1, qt1, st1 = fq().gated_backward(dh[n:m], Y[n:m], act=act, mode=mode)
+        assert torch.equal(q1, q[n:m]) and torch.equal(s1, s[:, n:m])
+        assert torch.equal(qt1, qt[:, n:n + qt1.shape[1]])
+        assert torch.equal(st1, st[n // 128:n // 128 + st1.shape[0]])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 def test_gated_backward_against_differences(act):
     """The dequantized dY against central differences of the forward formula:
     codes are within 2^-4 of the value, or 2^-10 of the group's scale's 448."""
