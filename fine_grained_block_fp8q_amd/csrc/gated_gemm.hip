@@ -6,7 +6,10 @@
 // chunk: gate and up rows lie in two weight blocks).  What the fused epilogue
 // saves is the 2F sums of a token written and read again, 8 bytes a sum in
 // FP32, and a launch: at 4096 tokens, F = 2048, that is 134 MB, 27 us at the
-// rate of a large copy beside a product of about 115.
+// rate of a large copy.  There, K = 7168: 101 us, 2.38 PFLOP/s (fp8q_gemm with
+// its 67 MB of FP32 results takes 115), 108 with Y saved; bound as the GEMM is,
+// by the promotion and the fragment reads beside the matrix core.  By expert
+// the weights' bytes bound it: 32 experts, 4300 rows 206 to 211 us, 973 MB.
 
 #include "grouped_gemm.hpp"
 #include "tile_choice.hpp"
@@ -100,10 +103,10 @@ hipError_t launch_gated_few(const uint8_t* a_q, const float* a_s, int64_t M, con
 // Kernel times with F = 2048 (4096 weight rows), K = 7168, in us, by number of
 // rows:
 //   rows          1     32    64    128   256   512   1024  2048  4096
-//   few rows      7.3   8.3   10.9  17    32
-//   64 x 128                  24.5  24.4  24.5  27.6  44    83    157
-//   128 x 128                 43    46    46    46    48.5  65    126
-//   256 x 256                       58    79    79    79.5  82    104
+//   few rows      7.2   7.8   10.8  16.7  32
+//   64 x 128                  24.2  24.2  24.5  26    40    79    157
+//   128 x 128                 43    46    46    46    46    64    126
+//   256 x 256                       58    79    79    79    82    101
 constexpr TileVariant kGatedVariants[] = {{64, 64, 128, 3380, 350, 388, 619, 1210, 1.0},
                                           {128, 128, 128, 3350, 596, 763, 948, 1430, 1.0},
                                           {256, 256, 256, 0, 1280, 1480, 2958, 7800, 1.0}};
