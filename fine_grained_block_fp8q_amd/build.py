@@ -106,7 +106,7 @@ def _build_calls(verbose):
                 "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
                 "-isystem", os.path.join(rocm, "include"), os.path.join(CSRC, "calls.cpp"),
                 "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
-                "-lc10_hip", "-o", tmp])
+                "-lc10_hip", "-ltorch_hip", "-o", tmp])
     if verbose and out.strip():
         print(out)
     os.replace(tmp, LIB_CALLS)
