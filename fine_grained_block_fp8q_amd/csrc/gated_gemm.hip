@@ -16,11 +16,17 @@
 
 namespace fp8q {
 
-// 256 x 256: the dense GEMM's tile.  128 x 128 and 64 x 128: for batches that
-// have too few of the larger tiles to fill the CUs.
+// 256 x 256: the dense GEMM's tile.  The others are for batches that have too
+// few of it to fill the CUs; their third stage is worth 46 -> 31 us at 512 rows
+// (128 x 128, with 8 waves for 4), beside the second workgroup on a CU that it
+// takes the room of.
 using Gated256 = GemmCfg<256, 256, 4, 2, 2, 256, 1, kOpFp8, 0, 0, 1>;
-using Gated128 = GemmCfg<128, 128, 2, 2, 2, 128, 0, kOpFp8, 0, 0, 1>;
+using Gated256x128 = GemmCfg<256, 128, 4, 2, 3, 256, 0, kOpFp8, 0, 0, 1>;
+using Gated128 = GemmCfg<128, 128, 2, 4, 3, 128, 0, kOpFp8, 0, 0, 1>;
 using Gated64 = GemmCfg<64, 128, 1, 4, 3, 64, 0, kOpFp8, 0, 0, 1>;
+
+// The tile's rows of activations and of weights, in one number.
+constexpr int tile_id(int bm, int bn) { return 1000 * bm + bn; }
 
 template <class Cfg>
 __global__ __launch_bounds__(Cfg::THREADS) void gated_kernel(
@@ -65,9 +71,10 @@ static hipError_t launch_gated(const uint8_t* a_q, const float* a_s, int64_t M, 
 hipError_t launch_gated_tiles(const uint8_t* a_q, const float* a_s, int64_t M, const uint8_t* w_q,
                               const float* w_s, int64_t F, int64_t K, int act, void* h,
                               int out_bf16, void* gu, int tile, hipStream_t stream) {
-  auto launch = tile == 256   ? launch_gated<Gated256>
-                : tile == 128 ? launch_gated<Gated128>
-                              : launch_gated<Gated64>;
+  auto launch = tile == tile_id(256, 256)   ? launch_gated<Gated256>
+                : tile == tile_id(256, 128) ? launch_gated<Gated256x128>
+                : tile == tile_id(128, 128) ? launch_gated<Gated128>
+                                            : launch_gated<Gated64>;
   return launch(a_q, a_s, M, w_q, w_s, F, K, act, h, out_bf16, gu, stream);
 }
 
@@ -105,12 +112,15 @@ hipError_t launch_gated_few(const uint8_t* a_q, const float* a_s, int64_t M, con
 //   rows          1     32    64    128   256   512   1024  2048  4096
 //   few rows      7.2   7.8   10.8  16.7  32
 //   64 x 128                  24.2  24.2  24.5  26    40    79    157
-//   128 x 128                 43    46    46    46    46    64    126
-//   256 x 256                       58    79    79    79    82    101
-constexpr TileVariant kGatedVariants[] = {{64, 64, 128, 3380, 350, 388, 619, 1210, 1.0},
-                                          {128, 128, 128, 3350, 596, 763, 948, 1430, 1.0},
-                                          {256, 256, 256, 0, 1280, 1480, 2958, 7800, 1.0}};
-constexpr FewRowsCost kGatedFew = {3380, 1.28, 1.59, 18.3, 1.0};
+//   128 x 128                       31    31    31    35    68
+//   256 x 128                             48    48    49    56    112
+//   256 x 256                       58    79    79    79    80    100
+constexpr TileVariant kGatedVariants[] = {
+    {tile_id(64, 128), 64, 128, 3340, 350, 390, 601, 1260, 1.0},
+    {tile_id(128, 128), 128, 128, 950, 441, 530, 982, 3900, 1.0},
+    {tile_id(256, 128), 256, 128, 0, 713, 814, 1587, 6000, 1.0},
+    {tile_id(256, 256), 256, 256, 0, 1277, 1454, 2903, 7800, 1.0}};
+constexpr FewRowsCost kGatedFew = {3400, 1.27, 1.59, 17.8, 1.0};
 
 // off NULL: one dense block of weights; else G experts.
 hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, const int32_t* off,

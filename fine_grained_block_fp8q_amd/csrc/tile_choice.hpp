@@ -29,7 +29,7 @@ struct FewRowsCost {
 // fitted to measured times of every kernel at random shapes (M 33 to 5800,
 // weight rows 64 to 8192, K 128 to 9000).  Against the best kernel of each
 // shape the choice costs 1.1% on average and 16% at most over 156 int8 shapes,
-// 0.2% and 12% over 138 E4M3 ones.
+// 0.1% and 15% over 138 E4M3 ones.
 template <int N>
 inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few, int64_t M,
                         int64_t weight_rows, int64_t K, int step, int cus) {

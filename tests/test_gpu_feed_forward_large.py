@@ -134,6 +134,13 @@ def test_gemm_gated_tiles_form_the_gemms_sums(M, F, K, act):
         assert torch.equal(_bits(f.gemm_gated(a, sa, w, sw, act=act, out_dtype=out)), _bits(h))
 
 
+# 128 x 128 and 256 x 128 tiles, one row in the last of them
+@pytest.mark.parametrize("M,F,K,act", [(641, 2048, 512, "gelu_tanh"), (900, 2048, 256, "silu"),
+                                       (1537, 1664, 512, "gelu_tanh"), (2048, 2048, 1664, "silu")])
+def test_gemm_gated_middle_tiles_form_the_gemms_sums(M, F, K, act):
+    test_gemm_gated_tiles_form_the_gemms_sums(M, F, K, act)
+
+
 def test_grouped_gemm_gated_forms_the_grouped_gemms_sums():
     """Every row-count bucket of the grouped kernel, empty experts among them."""
     f, g = fq(), _gen(7)
