@@ -60,10 +60,11 @@ struct I8Cfg {
   static_assert(WM % 16 == 0 && WN % (GATED ? 32 : 16) == 0, "whole blocks");
   static_assert(NA * LA + NW * LW < 64, "loads in flight");
   static_assert(LDS <= 160 * 1024, "LDS budget");
-  // row blocks of outputs that a wave's share of the ring holds
-  static constexpr int ROW_BLOCKS = BF16 || WNO < 128 ? MB : MB / 2;
-  static_assert(LDS / NWAVES >= ROW_BLOCKS * 16 * (WNO * (BF16 ? 2 : 4) + 16) + WN * 8,
-                "they fit it, with the columns' scales");
+  // row blocks of outputs that a wave's share of the ring holds, with the
+  // columns' scales: all of them or half
+  static constexpr int share(int blocks) { return blocks * 16 * (WNO * (BF16 ? 2 : 4) + 16) + WN * 8; }
+  static constexpr int ROW_BLOCKS = share(MB) <= LDS / NWAVES ? MB : MB / 2;
+  static_assert(share(ROW_BLOCKS) <= LDS / NWAVES, "they fit it");
 };
 
 struct I8Args {
@@ -374,10 +375,13 @@ static hipError_t launch_tiles(I8Args p, hipStream_t stream) {
 
 template <bool GATED, bool BF16>
 static hipError_t launch_tile(const I8Args& p, int tile, hipStream_t stream) {
-  return tile == 256   ? launch_tiles<I8Cfg<256, 256, 2, 2, 2, GATED, BF16>>(p, stream)
-         : tile == 128 ? launch_tiles<I8Cfg<128, 128, 2, 2, 2, GATED, BF16>>(p, stream)
-         : tile == 64  ? launch_tiles<I8Cfg<64, 64, 2, 1, 3, GATED, BF16>>(p, stream)
-                       : launch_tiles<I8Cfg<32, 64, 1, 2, 3, GATED, BF16>>(p, stream);
+  switch (tile) {
+    case tile_id(256, 256): return launch_tiles<I8Cfg<256, 256, 2, 2, 2, GATED, BF16>>(p, stream);
+    case tile_id(256, 128): return launch_tiles<I8Cfg<256, 128, 2, 2, 2, GATED, BF16>>(p, stream);
+    case tile_id(128, 128): return launch_tiles<I8Cfg<128, 128, 2, 2, 2, GATED, BF16>>(p, stream);
+    case tile_id(64, 64): return launch_tiles<I8Cfg<64, 64, 2, 1, 3, GATED, BF16>>(p, stream);
+    default: return launch_tiles<I8Cfg<32, 64, 1, 2, 3, GATED, BF16>>(p, stream);
+  }
 }
 
 hipError_t launch_i8_tiles(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
@@ -411,15 +415,18 @@ hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q,
 //   32 x 64       14.2  14.3  18.3  31
 //   64 x 64       17.0  17.1  17.5  21.6  21.5  39    43
 //   128 x 128     23.6  24.7  24.7  24.9  25.2  26.1  28.6  52    108
+//   256 x 128                             38          41    50    102
 //   256 x 256           68    68    68    69    69    69    70    86-90
 // (64 x 128 tiles take 18.6 to 20.5 us up to 512 rows: with them beside the four
 // kept, 0.3% less time over 160 random shapes.)  The two smallest have rings of
 // three chunks of A and four of W and share a CU.
-constexpr TileVariant kI8Variants[] = {{32, 32, 64, 2680, 182, 189, 255, 640, 1.13},
-                                       {64, 64, 64, 2490, 229, 249, 299, 1260, 1.17},
-                                       {128, 128, 128, 2770, 320, 426, 758, 2350, 1.23},
-                                       {256, 256, 256, 4840, 1012, 1129, 2372, 8300, 1.09}};
-constexpr FewRowsCost kI8Few = {3130, 1.17, 1.74, 11.4, 1.1};
+constexpr TileVariant kI8Variants[] = {
+    {tile_id(32, 64), 32, 64, 2750, 179, 185, 255, 620, 1.15},
+    {tile_id(64, 64), 64, 64, 2510, 228, 251, 306, 1250, 1.19},
+    {tile_id(128, 128), 128, 128, 3000, 321, 398, 844, 2130, 1.18},
+    {tile_id(256, 128), 256, 128, 1850, 551, 739, 1435, 6200, 1.19},
+    {tile_id(256, 256), 256, 256, 5210, 972, 1147, 2418, 8110, 1.07}};
+constexpr FewRowsCost kI8Few = {2350, 1.12, 1.65, 10.4, 1.07};
 
 static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                             const float* w_s, const float* bias, int64_t M, int64_t N, int64_t K,

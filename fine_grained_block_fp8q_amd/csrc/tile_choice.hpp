@@ -5,6 +5,9 @@
 
 namespace fp8q {
 
+// A tile's rows of activations and of weights, in one number.
+constexpr int tile_id(int bm, int bn) { return 1000 * bm + bn; }
+
 // A tiled kernel's times in ns, its launch and the ring's first fill included
 // in `start`: for each 128 k with up to half of the CUs at work, with one
 // workgroup on each CU and with two (they overlap where two fit, else they
@@ -19,7 +22,7 @@ struct TileVariant {
 // The kernel for few rows: a workgroup of it holds 16 weight rows and 64 or 128
 // activation rows and its 8 waves take a chunk each.  In ns, for each of those
 // activation rows: a chunk with up to half of the CUs at work and with all, and
-// each further round of workgroups.
+// each round of workgroups.
 struct FewRowsCost {
   double start, idle, one, round, split;
 };
@@ -28,8 +31,9 @@ struct FewRowsCost {
 // for few rows does; the tiles take K in steps of `step`.  The constants are
 // fitted to measured times of every kernel at random shapes (M 33 to 5800,
 // weight rows 64 to 8192, K 128 to 9000).  Against the best kernel of each
-// shape the choice costs 1.1% on average and 16% at most over 156 int8 shapes,
-// 0.1% and 15% over 138 E4M3 ones.
+// shape the choice costs 0.6% on average and 16% at most over 200 int8 shapes,
+// 0.2% and 15% over 138 E4M3 ones; over 40 of both that were not fitted, 1.6%
+// and 18%.
 template <int N>
 inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few, int64_t M,
                         int64_t weight_rows, int64_t K, int step, int cus) {
@@ -41,9 +45,9 @@ inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few
   const int64_t rounds = blocks(n_few, cus);
   const bool idle = 2 * (n_few - (rounds - 1) * cus) <= cus;
   const double few_k = (double)(blocks(K, 1024) * 8) * (whole ? 1.0 : few.split);
-  double least =
-      few.start + (double)rows * (few_k * ((double)(rounds - 1) * few.one + (idle ? few.idle : few.one)) +
-                                  (double)(rounds - 1) * few.round);
+  double least = few.start + (double)rows * (few_k * ((double)(rounds - 1) * few.one +
+                                                      (idle ? few.idle : few.one)) +
+                                             (double)rounds * few.round);
   const double chunks = (double)(blocks(K, step) * step) / 128.0;
   int best = 0;
   for (const TileVariant& v : variants) {

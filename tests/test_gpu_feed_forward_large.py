@@ -100,6 +100,18 @@ def test_gemm_i8_gated_small_tiles(M, F, K, act):
     test_gemm_i8_gated_tiles(M, F, K, act)
 
 
+# 256 x 128 tiles
+@pytest.mark.parametrize("M,N,K,bias", [(1793, 4001, 1808, True), (2048, 4096, 2064, False)])
+def test_gemm_i8_middle_tiles(M, N, K, bias):
+    for out in (torch.bfloat16, torch.float32):
+        test_gemm_i8_tiles(M, N, K, bias, out)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_gemm_i8_gated_middle_tiles(act):
+    test_gemm_i8_gated_tiles(1793, 2005, 1808, act)
+
+
 def _codes(g, *shape):
     """E4M3 codes of finite values."""
     return torch.randint(0, 127, shape, generator=g, device=DEV, dtype=torch.uint8) \
