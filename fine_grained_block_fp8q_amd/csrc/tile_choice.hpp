@@ -19,8 +19,8 @@ struct TileVariant {
   double start, idle, one, two, end, split;
 };
 
-// The kernel for few rows: a workgroup of it holds 16 weight rows and 64 or 128
-// activation rows and its 8 waves take a chunk each.  In ns, for each of those
+// The kernel for few rows: a workgroup of it holds 16 weight rows and 32, 64 or
+// 128 activation rows and its 8 waves take a chunk each.  In ns, for each of those
 // activation rows: a chunk with up to half of the CUs at work and with all, and
 // each round of workgroups.
 struct FewRowsCost {
@@ -33,14 +33,15 @@ struct FewRowsCost {
 // weight rows 64 to 8192, K 128 to 9000).  Against the best kernel of each
 // shape the choice costs 0.6% on average and 16% at most over 200 int8 shapes,
 // 0.2% and 15% over 138 E4M3 ones; over 40 of both that were not fitted, 1.6%
-// and 18%.
+// and 18%.  (With 17 to 32 rows it matters where weight rows make several rounds
+// of few-row workgroups: 32 x 32768 x 512 takes 10.4 us in those, 6.8 in tiles.)
 template <int N>
 inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few, int64_t M,
                         int64_t weight_rows, int64_t K, int step, int cus) {
   auto blocks = [](int64_t x, int64_t b) { return (x + b - 1) / b; };
-  if (M <= 32) return 0;
+  if (M <= 16) return 0;
   const bool whole = K % 128 == 0;
-  const int64_t rows = M <= 64 ? 64 : 128;
+  const int64_t rows = M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const int64_t n_few = blocks(M, rows) * blocks(weight_rows, 16);
   const int64_t rounds = blocks(n_few, cus);
   const bool idle = 2 * (n_few - (rounds - 1) * cus) <= cus;

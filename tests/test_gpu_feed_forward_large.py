@@ -87,7 +87,8 @@ def test_gemm_i8_gated_tiles(M, F, K, act):
 # K and part of it, chunks that end inside the ring's first round
 @pytest.mark.parametrize("M,N,K,bias", [(33, 70, 16, True), (65, 300, 1040, False),
                                         (333, 1100, 1040, True), (500, 2051, 336, False),
-                                        (449, 2001, 400, True), (129, 513, 2064, False)])
+                                        (449, 2001, 400, True), (129, 513, 2064, False),
+                                        (17, 16390, 256, True), (32, 16384, 144, False)])
 def test_gemm_i8_small_tiles(M, N, K, bias):
     for out in (torch.bfloat16, torch.float32):
         test_gemm_i8_tiles(M, N, K, bias, out)
@@ -95,7 +96,7 @@ def test_gemm_i8_small_tiles(M, N, K, bias):
 
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("M,F,K", [(33, 35, 144), (97, 150, 1040), (450, 1000, 336),
-                                   (513, 1025, 528)])
+                                   (513, 1025, 528), (20, 8200, 256)])
 def test_gemm_i8_gated_small_tiles(M, F, K, act):
     test_gemm_i8_gated_tiles(M, F, K, act)
 
