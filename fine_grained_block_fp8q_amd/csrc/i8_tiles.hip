@@ -254,8 +254,9 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
 #pragma unroll
   for (int j = 0; j < NB; ++j) read_w(w0[j], 0, 0, j);
   lds_barrier();  // A's unit of chunk 0 is read
-  int t = 0, u = 0;
-  for (int g = 0; g < chunks; g += 2) {
+  int t = 0, u = 0, g = 0;
+  do {  // (K >= 1: at least one pair.  With a way past the loop the sums would be
+        // copied to common registers behind it, ahead of the wait below.)
     const int t1 = t + 1 == Cfg::NA ? 0 : t + 1, t2 = t1 + 1 == Cfg::NA ? 0 : t1 + 1;
     const int u1 = u + 1 == Cfg::NW ? 0 : u + 1, u2 = u1 + 1 == Cfg::NW ? 0 : u1 + 1;
     step0(g, t, u);
@@ -264,7 +265,16 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
     step1(g + 1, a1[1], a1[0], t2, u1, u2);
     t = t2;
     u = u2;
-  }
+    g += 2;
+  } while (g < chunks);
+  // The last products' results, before anything else uses them: the products
+  // are inline asm, of which the compiler knows no latency.  The sums are made
+  // outputs of statements behind the wait, so that no use can move ahead of it.
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) asm volatile("" : "+a"(acc[i][j]));
   // The rows' and columns' scales and the bias, for the epilogue.  (Asked for
   // before the loop they would be spilled there, each with a wait of its own.)
   constexpr int CS = (Cfg::WN + 63) / 64;
@@ -282,8 +292,6 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
     const int64_t m = m0 + wave_m * Cfg::WM + 16 * i + fr;
     row_scale[i] = p.a_s[m < p.M ? m : p.M - 1];
   }
-  // the last products' results, before the vector ALU reads them
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
   wait_vmcnt<0>();
   lds_barrier();  // the ring is free: each wave takes its share for its output rows
 
