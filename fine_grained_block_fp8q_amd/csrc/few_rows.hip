@@ -30,6 +30,7 @@
 
 #include "activation.hpp"
 #include "gemm_common.hpp"
+#include "launch.hpp"
 
 namespace fp8q {
 
@@ -47,7 +48,8 @@ struct FewArgs {
   void* c;             // [M][N], or h [M][F]
   uint16_t* gu;        // gated: Y as BF16 [M][2F], or NULL
   int64_t M, N, K;     // N: output columns (F when gated)
-  int n_blocks;        // column blocks
+  int n_blocks;        // column blocks of this launch,
+  int n_first;         // and the first of them
   int out_bf16, act;
 };
 
@@ -70,7 +72,7 @@ __device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4;
-  const int nb = blockIdx.x % p.n_blocks, mb = blockIdx.x / p.n_blocks;
+  const int nb = p.n_first + blockIdx.x % p.n_blocks, mb = blockIdx.x / p.n_blocks;
 
   const int64_t r0 = (int64_t)mb * BM;
   const int64_t K = p.K, N = p.N;
@@ -244,14 +246,21 @@ static hipError_t launch_few(FewArgs p, hipStream_t stream) {
   const int64_t n_blocks = (p.N + NCOL - 1) / NCOL;
   const int MB = p.M <= 16 ? 1 : p.M <= 32 ? 2 : p.M <= 64 ? 4 : 8;
   const int64_t m_blocks = (p.M + 16 * MB - 1) / (16 * MB);
-  if (n_blocks * m_blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  p.n_blocks = (int)n_blocks;
+  const int64_t slice = max_blocks(kFewThreads) / m_blocks;  // column blocks a launch
+  if (slice == 0 || n_blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   auto kern = MB == 1   ? few_rows_kernel<OP, 1, GATED>
               : MB == 2 ? few_rows_kernel<OP, 2, GATED>
               : MB == 4 ? few_rows_kernel<OP, 4, GATED>
                         : few_rows_kernel<OP, 8, GATED>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(n_blocks * m_blocks)), dim3(kFewThreads), 0, stream, p);
-  return hipGetLastError();
+  for (int64_t b = 0; b < n_blocks; b += slice) {
+    p.n_first = (int)b;
+    p.n_blocks = (int)(n_blocks - b < slice ? n_blocks - b : slice);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(p.n_blocks * m_blocks)), dim3(kFewThreads), 0, stream,
+                       p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,

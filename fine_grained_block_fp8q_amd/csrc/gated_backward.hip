@@ -39,6 +39,7 @@
 
 #include "activation.hpp"
 #include "gemm_common.hpp"
+#include "launch.hpp"
 #include "quant_rules.hpp"
 
 namespace fp8q {
@@ -378,7 +379,7 @@ hipError_t launch_gated_backward(const void* dh, const void* gu, int64_t M, int6
                                  int mode, uint8_t* q, float* s, uint8_t* qt, float* st,
                                  hipStream_t stream) {
   const int64_t n_fblk = F / kGroup, tb = (M + kGroup - 1) / kGroup;
-  if (n_fblk * tb > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (n_fblk * tb > max_blocks(kBwThreads)) return hipErrorInvalidValue;
   if (n_fblk * tb <= kSmallBlocks) {
     const int64_t n_rows = q ? (M + kRowsTokens - 1) / kRowsTokens * n_fblk : 0;
     const int64_t n = n_rows + (qt ? tb * n_fblk * (kGroup / kTokensFeatures) : 0);

@@ -12,6 +12,7 @@
 // the weights' bytes bound it: 32 experts, 4300 rows 206 to 211 us, 973 MB.
 
 #include "grouped_gemm.hpp"
+#include "launch.hpp"
 #include "tile_choice.hpp"
 
 namespace fp8q {
@@ -58,7 +59,7 @@ static hipError_t launch_gated(const uint8_t* a_q, const float* a_s, int64_t M, 
                                const float* w_s, int64_t F, int64_t K, int act, void* h,
                                int out_bf16, void* gu, hipStream_t stream) {
   const int64_t tiles_n = F / (Cfg::BN / 2), tiles = (M + Cfg::BM - 1) / Cfg::BM * tiles_n;
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (tiles > max_blocks(Cfg::THREADS)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(gated_kernel<Cfg>, dim3((unsigned)tiles), dim3(Cfg::THREADS), 0, stream, a_q,
                      a_s, w_q, w_s, M, F, K, h, out_bf16, static_cast<uint16_t*>(gu), act,
                      (int)tiles_n);

@@ -36,6 +36,7 @@
 
 #include "activation.hpp"
 #include "gemm_common.hpp"
+#include "launch.hpp"
 #include "tile_choice.hpp"
 
 namespace fp8q {
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void i8_tile_kernel(const I8Args p) {
 template <class Cfg>
 static hipError_t launch_tiles(I8Args p, hipStream_t stream) {
   const int64_t tiles_m = (p.M + Cfg::BM - 1) / Cfg::BM, tiles_n = (p.N + Cfg::OBN - 1) / Cfg::OBN;
-  if (tiles_m * tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (tiles_m * tiles_n > max_blocks(Cfg::THREADS)) return hipErrorInvalidValue;
   p.tiles_n = (int)tiles_n;
   hipLaunchKernelGGL(i8_tile_kernel<Cfg>, dim3((unsigned)(tiles_m * tiles_n)), dim3(Cfg::THREADS), 0,
                      stream, p);

@@ -14,6 +14,7 @@
 // flushed: s = 0 and every code 0.
 
 #include "fp8q_device.hpp"
+#include "launch.hpp"
 
 namespace fp8q {
 
@@ -103,9 +104,7 @@ __global__ __launch_bounds__(256) void quantize_token_i8_kernel(const uint16_t* 
 
 hipError_t launch_quantize_token_i8(const void* x, int64_t M, int64_t K, int64_t Kp, int8_t* q,
                                     float* s, hipStream_t stream) {
-  const bool wave_rows = K <= 2048;
-  const int64_t blocks = wave_rows ? (M + 3) / 4 : M;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int rows = K <= 2048 ? 4 : 1;  // of a workgroup
   auto kern = K <= 512      ? quantize_token_i8_kernel<64, 1>
               : K <= 1024   ? quantize_token_i8_kernel<64, 2>
               : K <= 2048   ? quantize_token_i8_kernel<64, 4>
@@ -113,9 +112,15 @@ hipError_t launch_quantize_token_i8(const void* x, int64_t M, int64_t K, int64_t
               : K <= 8192   ? quantize_token_i8_kernel<256, 4>
               : K <= 16384  ? quantize_token_i8_kernel<256, 8>
                             : quantize_token_i8_kernel<256, 0>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, stream,
-                     static_cast<const uint16_t*>(x), M, K, Kp, q, s);
-  return hipGetLastError();
+  const int64_t slice = rows * max_blocks(256);
+  for (int64_t r = 0; r < M; r += slice) {
+    const int64_t n = M - r < slice ? M - r : slice;
+    hipLaunchKernelGGL(kern, dim3((unsigned)((n + rows - 1) / rows)), dim3(256), 0, stream,
+                       static_cast<const uint16_t*>(x) + r * K, n, K, Kp, q + r * Kp, s + r);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp8q
