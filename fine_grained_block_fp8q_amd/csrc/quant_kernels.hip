@@ -16,6 +16,7 @@
 // quant_rules.hpp; this file is built without fast math and without FP
 // contraction.
 
+#include "launch.hpp"
 #include "quant_rules.hpp"
 
 namespace fp8q {
@@ -281,7 +282,7 @@ hipError_t launch_quantize_act_t(const void* x, int64_t M, int64_t K, uint8_t* q
   const int64_t n_kblk = K / 64;
   const int64_t blocks = (M / kGroup) * n_kblk;
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks > max_blocks(256)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
   if (mode == 0)
     hipLaunchKernelGGL(quantize_act_t_kernel<0>, grid, block, 0, stream,
@@ -297,7 +298,7 @@ hipError_t launch_quantize_weight_t(const void* w, int64_t N, int64_t K, uint8_t
   const int64_t KB = K / kGroup;
   const int64_t blocks = (N / kGroup) * KB;
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks > max_blocks(256)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
   if (mode == 0)
     hipLaunchKernelGGL(quantize_weight_t_kernel<0>, grid, block, 0, stream,
@@ -315,7 +316,7 @@ hipError_t launch_quantize_act(const void* x, int64_t M, int64_t K, uint8_t* q, 
   const int64_t n_rblk = (M + kActRows - 1) / kActRows;
   const int64_t blocks = n_gblk * n_rblk;
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks > max_blocks(256)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
   if (mode == 0)
     hipLaunchKernelGGL(quantize_act_kernel<0>, grid, block, 0, stream,
@@ -331,7 +332,7 @@ hipError_t launch_quantize_weight(const void* w, int64_t N, int64_t K, uint8_t* 
   const int64_t KB = K / kGroup;
   const int64_t blocks = (N / kGroup) * KB;
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks > max_blocks(256)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
   if (mode == 0)
     hipLaunchKernelGGL(quantize_weight_kernel<0>, grid, block, 0, stream,

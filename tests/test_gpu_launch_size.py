@@ -71,3 +71,20 @@ def test_few_rows_e4m3():
         b = torch.tensor([f0 // 128, (F + f0) // 128], device=DEV)
         assert torch.equal(h[:, f0:f0 + 128],
                            f.gemm_gated(a, sa, w[r], sw[b], out_dtype=torch.float32)), f0
+
+
+def test_quantize_act_refuses_what_one_launch_cannot_take():
+    """16 rows of one group to a workgroup of 256 lanes: 2^28 rows are past the limit."""
+    f = fq()
+    M = (1 << 28) + 16
+    x = torch.empty((M, 128), dtype=torch.bfloat16, device=DEV)
+    q = torch.empty((M, 128), dtype=torch.uint8, device=DEV)
+    s = torch.empty((1, M), dtype=torch.float32, device=DEV)
+    with pytest.raises(f.Fp8qError, match="ERR_LAUNCH"):
+        f.fp8q_quantize_act(x, q, s)
+    # the most that is taken
+    m = M - 32
+    x[:m] = 1
+    s = torch.zeros((1, m), dtype=torch.float32, device=DEV)
+    f.fp8q_quantize_act(x[:m], q[:m], s)
+    assert bool((s == s[0, 0]).all()) and float(s[0, 0]) > 0
