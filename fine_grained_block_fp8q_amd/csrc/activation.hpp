@@ -22,14 +22,17 @@ __device__ __forceinline__ float act_arg(int act, float x) {
   return act == kActSilu ? x : x * (kGelu1 + kGelu3 * x * x);
 }
 
-// act(x), for a result that is rounded to BF16 or used in FP32 beside a
-// matrix product's own FP32 rounding: the hardware exponential and reciprocal
-// (each within 1 unit in the last place of FP32, the exponential's argument
-// scaled by log2 e) are far inside both.  The reciprocal delivers no subnormal
-// numbers; with 1 + e scaled by 2^-16 it need not for any finite e.
+// act(x), for a result that is rounded to BF16 or used in FP32 beside a matrix
+// product's own FP32 rounding: the hardware exponential and reciprocal, each
+// within 1 unit in the last place of FP32, and an exponent that is off by the
+// rounding of y and of its product with log2 e, (16 + 8|y|) 2^-24 of act(x) in
+// all.  With 1 + e scaled by 2^-16 the reciprocal of any finite e is a normal
+// number (it delivers no subnormal ones); e is infinite, and act(x) taken as 0,
+// from y = -88.7 on.  The scale is taken off the reciprocal, not put on x, which
+// may be as small as there are numbers.
 __device__ __forceinline__ float act_fast(int act, float x) {
   const float e = __builtin_amdgcn_exp2f(act_arg(act, x) * -1.4426950408889634f);
-  return (x * 0x1p-16f) * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0x1p-16f, 0x1p-16f));
+  return x * (__builtin_amdgcn_rcpf(__builtin_fmaf(e, 0x1p-16f, 0x1p-16f)) * 0x1p-16f);
 }
 
 // act(x) and act'(x) to a few FP32 units: their results are quantized, and a

@@ -411,7 +411,8 @@ fp8q_status fp8q_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t
  *         h is formed from the FP32 Y, not from this rounded copy.
  *   M >= 0, F % 128 == 0, K % 128 == 0; errors as fp8q_gemm.
  * act(x) = x sigma(y) (y = x, or 2 sqrt(2/pi) (x + 0.044715 x^3)) is evaluated
- * in FP32 with an error of at most (16 + 8|y|) 2^-24 |act(x)| + 2^-128 |x|.
+ * in FP32 with an error of at most (16 + 8|y|) 2^-24 |act(x)| + 2^-128 |x| +
+ * 2^-149.
  */
 fp8q_status fp8q_gemm_gated(const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
                             const float* w_s, int64_t M, int64_t F, int64_t K,
