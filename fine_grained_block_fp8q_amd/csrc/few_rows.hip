@@ -221,7 +221,8 @@ __device__ __forceinline__ void few_rows(const FewArgs& p, uint8_t* smem) {
         g = total(m, c);
         u = total(m, c + 8);
       }
-      store(p.c, row * N + n, act_fast(p.act, g) * u, p.out_bf16);
+      const float h = (I8 && !p.out_bf16 ? act_f32(p.act, g) : act_fast(p.act, g)) * u;
+      store(p.c, row * N + n, h, p.out_bf16);
       if (p.gu) {
         store(p.gu, row * 2 * N + n, g, 1);
         store(p.gu, row * 2 * N + N + n, u, 1);

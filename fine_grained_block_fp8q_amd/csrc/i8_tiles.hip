@@ -332,11 +332,13 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, uint8_t* smem) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[e] = (float)acc[i][j][e] * row_scale[i];
-          if constexpr (Cfg::GATED)
-            v[e] = act_fast(p.act, v[e] * s_w[j][e]) *
+          if constexpr (Cfg::GATED) {
+            const float g = v[e] * s_w[j][e];
+            v[e] = (Cfg::BF16 ? act_fast(p.act, g) : act_f32(p.act, g)) *
                    ((float)acc[i][j + NB / 2][e] * row_scale[i] * more[j][e]);
-          else
+          } else {
             v[e] = __builtin_fmaf(v[e], s_w[j][e], more[j][e]);
+          }
         }
         uint8_t* at = rows + (16 * (i - i0) + fr) * PITCH + (16 * j + 4 * fq) * OB;
         if constexpr (Cfg::BF16)

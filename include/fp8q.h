@@ -393,6 +393,9 @@ fp8q_status fp8q_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
  *   w_q : [2F][K] int8 (rows 0..F-1 gate, F..2F-1 up), w_s : [2F] float32
  *   h   : [M][F] float32 or bfloat16 (per `out`) (output).
  *   M >= 0, any F >= 0, K % 16 == 0; errors as fp8q_gemm_i8.
+ * act(x) = x sigma(y) (y = x, or 2 sqrt(2/pi) (x + 0.044715 x^3)) is evaluated
+ * in FP32 with an error of at most 2^-128 |x| + 2^-149 and, relative to |act(x)|,
+ * 8 * 2^-24 for FP32 output, (16 + 8|y|) 2^-24 for BF16 output.
  */
 fp8q_status fp8q_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                                const float* w_s, int64_t M, int64_t F, int64_t K,
@@ -410,9 +413,9 @@ fp8q_status fp8q_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t
  *   gate_up : [M][2F] bfloat16 Y for the backward pass (output), or NULL;
  *         h is formed from the FP32 Y, not from this rounded copy.
  *   M >= 0, F % 128 == 0, K % 128 == 0; errors as fp8q_gemm.
- * act(x) = x sigma(y) (y = x, or 2 sqrt(2/pi) (x + 0.044715 x^3)) is evaluated
- * in FP32 with an error of at most (16 + 8|y|) 2^-24 |act(x)| + 2^-128 |x| +
- * 2^-149.
+ * act(x) (as above) is evaluated in FP32 with an error of at most
+ * (16 + 8|y|) 2^-24 |act(x)| + 2^-128 |x| + 2^-149: the sums of the FP8 matrix
+ * cores carry more.
  */
 fp8q_status fp8q_gemm_gated(const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
                             const float* w_s, int64_t M, int64_t F, int64_t K,
