@@ -17,11 +17,13 @@ Allocation helpers (``quantize_act``, ``quantize_weight``, ``gemm``,
 then call the entry points.  Those of the feed-forward operators
 (``quantize_token_i8``, ``gemm_i8``, ``gemm_gated``, ...) do so in compiled code
 (csrc/calls.cpp) when every argument is as it should be and no stream is named;
-else they take the Python path, whose checks say what is wrong.
+else, and where the compiled module cannot be loaded, they take the Python path,
+whose checks say what is wrong.
 """
 
 import ctypes
 import os
+import warnings
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -31,9 +33,6 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"libfp8q.so not found at {LIB_PATH}; build it with "
         "`python fine_grained_block_fp8q_amd/build.py` (hipcc, gfx950)")
-
-if not os.path.exists(os.path.join(_PKG, "_calls.so")):
-    raise ImportError(f"_calls.so not found in {_PKG}; build it as libfp8q.so")
 
 lib = ctypes.CDLL(LIB_PATH)
 
@@ -650,18 +649,36 @@ def grouped_gemm(a_q, a_s, off, w_q, w_s, out_dtype=None, stream=None, precise=F
 _native = None
 
 
+class _PythonPath:
+    """In the compiled module's place: takes no call, so each goes the Python path."""
+
+    @staticmethod
+    def _decline(*args):
+        return None
+
+    quantize_token_i8 = gemm_i8 = gemm_i8_gated = gemm_gated = gated_backward = _decline
+
+
 def _compiled():
-    """The module of csrc/calls.cpp with this library's entry points, and the
-    output codes of the dtypes it allocates."""
+    """The module of csrc/calls.cpp with this library's entry points (or, where it
+    cannot be loaded, _PythonPath), and the output codes of the dtypes it
+    allocates."""
     global _native, _OUT_OF
     import torch       # its libraries first
-    from . import _calls
+    _OUT_OF = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+    try:
+        from . import _calls
+    except ImportError as e:   # not built, or against another torch
+        warnings.warn(f"the compiled calls cannot be loaded ({e}); the feed-forward helpers "
+                      "take their Python path, about 10 us a call slower", RuntimeWarning,
+                      stacklevel=3)
+        _native = _PythonPath
+        return _native
     _calls.entries(*(ctypes.cast(getattr(lib, "fp8q_" + n), _p).value for n in
                      ("quantize_token_i8", "gemm_i8", "gemm_i8_gated", "gemm_gated",
                       "grouped_gemm_gated", "gated_backward")))
-    _OUT_OF = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
     _native = _calls
-    return _calls
+    return _native
 
 
 def _refused(status, where):

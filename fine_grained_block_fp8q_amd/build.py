@@ -22,7 +22,8 @@ LIB_DEBUG = os.path.join(PKG, "libfp8q_debug.so")
 # and counter calibration); not part of the method's C ABI.
 LIB_PROBE = os.path.join(PKG, "libfp8q_probe.so")
 # The compiled calls of the Python package (a CPython module against torch's
-# headers; it gets the entry points' addresses from the package).
+# headers; it gets the entry points' addresses from the package).  Optional: built
+# where torch and g++ are found.
 LIB_CALLS = os.path.join(PKG, "_calls.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
@@ -95,9 +96,20 @@ def build(verbose=False):
 
 
 def _build_calls(verbose):
+    import shutil
     import sysconfig
-
-    import torch
+    try:
+        import torch
+    except ImportError:
+        torch = None
+    lacks = "torch" if torch is None else None if shutil.which("g++") else "g++"
+    if lacks:
+        # the library does without it; one of an earlier build would not match
+        if os.path.exists(LIB_CALLS):
+            os.remove(LIB_CALLS)
+        print(f"{lacks} not found: {os.path.basename(LIB_CALLS)} is not built, the Python "
+              "package's feed-forward helpers will take their Python path", flush=True)
+        return
     home = os.path.dirname(torch.__file__)
     rocm = os.path.dirname(os.path.dirname(HIPCC))
     tmp = LIB_CALLS + ".tmp"
