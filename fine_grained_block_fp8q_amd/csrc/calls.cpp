@@ -8,14 +8,20 @@
 // current device; the outputs are allocated, the C entry point called on torch's
 // current stream, and the outputs returned.  They return an int (the status)
 // when the entry point refuses, and None when an argument is not as it should
-// be: the Python function then takes its own path, whose checks raise.
+// be: the Python function then takes its own path, whose checks raise.  They
+// return None too while something is to see or fill torch's allocations (a
+// dispatch mode, or the deterministic filling of uninitialized memory), which
+// these do not show it.  (Function modes do not count: the default device is one,
+// and the allocations name theirs.)
 //
 // Nothing is kept from one call for the next.
 
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/Context.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -42,12 +48,19 @@ const Tensor* tensor(PyObject* o) {
   return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr;
 }
 
+bool allocations_watched() {
+  const auto& context = at::globalContext();
+  return c10::impl::TorchDispatchModeTLS::any_modes_set() ||
+         (context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory());
+}
+
 // Tensors of one call: all on the device of the first, which is current.
 struct Call {
   at::Device dev;
   bool ok;
   explicit Call(const Tensor& first)
-      : dev(first.device()), ok(dev.is_cuda() && dev.index() == c10::hip::current_device()) {}
+      : dev(first.device()),
+        ok(dev.is_cuda() && dev.index() == c10::hip::current_device() && !allocations_watched()) {}
   void need(const Tensor& t, at::ScalarType type, at::IntArrayRef sizes) {
     ok = ok && t.scalar_type() == type && t.device() == dev && t.sizes() == sizes &&
          t.is_contiguous();
