@@ -71,6 +71,13 @@ struct Call {
   hipStream_t stream() const { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 };
 
+// The truth of a flag; false with Python's error set where it has none.
+bool truth(PyObject* o, bool& value) {
+  const int t = PyObject_IsTrue(o);
+  value = t == 1;
+  return t >= 0;
+}
+
 template <class T = void>
 T* at_(const Tensor& t) {
   return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
@@ -214,7 +221,8 @@ PyObject* gemm_gated(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     if (!c.ok || K % 128 || N % 256 || G > INT32_MAX) Py_RETURN_NONE;
     const auto act = (fp8q_activation)PyLong_AsLong(args[5]);
     const int out = (int)PyLong_AsLong(args[6]);
-    const bool save = PyObject_IsTrue(args[7]) == 1;
+    bool save;
+    if (!truth(args[7], save)) return nullptr;
     const Tensor h = c.make(out_type(out), {M, N / 2});
     const Tensor gu = save ? c.make(at::kBFloat16, {M, N}) : Tensor();
     const fp8q_status st =
@@ -238,7 +246,8 @@ PyObject* gated_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     Call c(*dh);
     c.need(*dh, at::kBFloat16, {M, F});
     c.need(*gu, at::kBFloat16, {M, 2 * F});
-    const bool rows = PyObject_IsTrue(args[4]) == 1, tokens = PyObject_IsTrue(args[5]) == 1;
+    bool rows, tokens;
+    if (!truth(args[4], rows) || !truth(args[5], tokens)) return nullptr;
     if (!c.ok || F % 128 || !(rows || tokens)) Py_RETURN_NONE;
     Tensor q, s, qt, st;
     if (rows) {
