@@ -105,21 +105,6 @@ hipError_t launch_gated_few(const uint8_t* a_q, const float* a_s, int64_t M, con
                             const float* w_s, int64_t F, int64_t K, int act, void* h, int out_bf16,
                             void* gu, hipStream_t stream);
 
-// Kernel times with F = 2048 (4096 weight rows), K = 7168, in us, by number of
-// rows:
-//   rows          1     32    64    128   256   512   1024  2048  4096
-//   few rows      7.2   7.8   10.8  16.7  32
-//   64 x 128                  24.2  24.2  24.5  26    40    79    157
-//   128 x 128                       31    31    31    35    68
-//   256 x 128                             48    48    49    56    112
-//   256 x 256                       58    79    79    79    80    100
-constexpr TileVariant kGatedVariants[] = {
-    {tile_id(64, 128), 64, 128, 3340, 350, 390, 601, 1260, 1.0},
-    {tile_id(128, 128), 128, 128, 950, 441, 530, 982, 3900, 1.0},
-    {tile_id(256, 128), 256, 128, 0, 713, 814, 1587, 6000, 1.0},
-    {tile_id(256, 256), 256, 256, 0, 1277, 1454, 2903, 7800, 1.0}};
-constexpr FewRowsCost kGatedFew = {1970, 1.26, 1.59, 14.3, 1.0};
-
 // off NULL: one dense block of weights; else G experts.
 hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, const int32_t* off,
                              int G, const uint8_t* w_q, const float* w_s, int64_t F, int64_t K,
@@ -131,7 +116,7 @@ hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, co
   if (off)
     return launch_grouped_gated_tiles(a_q, a_s, M, off, G, w_q, w_s, F, K, act, h, out_bf16, gu,
                                       cus, stream);
-  const int tile = pick_variant(kGatedVariants, kGatedFew, M, 2 * F, K, 128, cus);
+  const int tile = pick_gated(M, 2 * F, K, cus);
   if (tile == 0)
     return launch_gated_few(a_q, a_s, M, w_q, w_s, F, K, act, h, out_bf16, gu, stream);
   return launch_gated_tiles(a_q, a_s, M, w_q, w_s, F, K, act, h, out_bf16, gu, tile, stream);

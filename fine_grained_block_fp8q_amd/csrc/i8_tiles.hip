@@ -420,25 +420,6 @@ hipError_t launch_i8_few(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                          const float* bias, int64_t M, int64_t N, int64_t K, bool gated, int act,
                          void* c, int out_bf16, hipStream_t stream);
 
-// Kernel times with 4096 weight rows, K = 7168, in us, by number of rows:
-//   rows          64    128   256   384   512   768   1024  2048  4096
-//   few rows      10.2  15.7  29
-//   32 x 64       14.2  14.3  18.3  31
-//   64 x 64       17.0  17.1  17.5  21.6  21.5  39    43
-//   128 x 128     23.6  24.7  24.7  24.9  25.2  26.1  28.6  52    108
-//   256 x 128                             38          41    50    102
-//   256 x 256           68    68    68    69    69    69    70    86-90
-// (64 x 128 tiles take 18.6 to 20.5 us up to 512 rows: with them beside the four
-// kept, 0.3% less time over 160 random shapes.)  The two smallest have rings of
-// three chunks of A and four of W and share a CU.
-constexpr TileVariant kI8Variants[] = {
-    {tile_id(32, 64), 32, 64, 2750, 179, 185, 255, 620, 1.15},
-    {tile_id(64, 64), 64, 64, 2510, 228, 251, 306, 1250, 1.19},
-    {tile_id(128, 128), 128, 128, 3000, 321, 398, 844, 2130, 1.18},
-    {tile_id(256, 128), 256, 128, 1850, 551, 739, 1435, 6200, 1.19},
-    {tile_id(256, 256), 256, 256, 5210, 972, 1147, 2418, 8110, 1.07}};
-constexpr FewRowsCost kI8Few = {2350, 1.12, 1.65, 10.4, 1.07};
-
 static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
                             const float* w_s, const float* bias, int64_t M, int64_t N, int64_t K,
                             bool gated, int act, void* c, int out_bf16, hipStream_t stream) {
@@ -446,7 +427,7 @@ static hipError_t launch_i8(const int8_t* a_q, const float* a_s, const int8_t* w
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
     return hipGetLastError();
-  const int tile = pick_variant(kI8Variants, kI8Few, M, gated ? 2 * N : N, K, 256, cus);
+  const int tile = pick_i8(M, gated ? 2 * N : N, K, cus);
   if (tile == 0)
     return launch_i8_few(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, stream);
   return launch_i8_tiles(a_q, a_s, w_q, w_s, bias, M, N, K, gated, act, c, out_bf16, tile, stream);

@@ -65,4 +65,48 @@ inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few
   return best;
 }
 
+// int8 products (i8_tiles.hip): kernel times with 4096 weight rows, K = 7168, in us, by number of rows:
+//   rows          64    128   256   384   512   768   1024  2048  4096
+//   few rows      10.2  15.7  29
+//   32 x 64       14.2  14.3  18.3  31
+//   64 x 64       17.0  17.1  17.5  21.6  21.5  39    43
+//   128 x 128     23.6  24.7  24.7  24.9  25.2  26.1  28.6  52    108
+//   256 x 128                             38          41    50    102
+//   256 x 256           68    68    68    69    69    69    70    86-90
+// (64 x 128 tiles take 18.6 to 20.5 us up to 512 rows: with them beside the four
+// kept, 0.3% less time over 160 random shapes.)  The two smallest have rings of
+// three chunks of A and four of W and share a CU.
+constexpr TileVariant kI8Variants[] = {
+    {tile_id(32, 64), 32, 64, 2750, 179, 185, 255, 620, 1.15},
+    {tile_id(64, 64), 64, 64, 2510, 228, 251, 306, 1250, 1.19},
+    {tile_id(128, 128), 128, 128, 3000, 321, 398, 844, 2130, 1.18},
+    {tile_id(256, 128), 256, 128, 1850, 551, 739, 1435, 6200, 1.19},
+    {tile_id(256, 256), 256, 256, 5210, 972, 1147, 2418, 8110, 1.07}};
+constexpr FewRowsCost kI8Few = {2350, 1.12, 1.65, 10.4, 1.07};
+
+// Rows, weight rows and K of an int8 product to its kernel.
+inline int pick_i8(int64_t M, int64_t weight_rows, int64_t K, int cus) {
+  return pick_variant(kI8Variants, kI8Few, M, weight_rows, K, 256, cus);
+}
+
+// The gated block on E4M3 operands (gated_gemm.hip): kernel times with F = 2048 (4096 weight rows), K = 7168, in us, by number of
+// rows:
+//   rows          1     32    64    128   256   512   1024  2048  4096
+//   few rows      7.2   7.8   10.8  16.7  32
+//   64 x 128                  24.2  24.2  24.5  26    40    79    157
+//   128 x 128                       31    31    31    35    68
+//   256 x 128                             48    48    49    56    112
+//   256 x 256                       58    79    79    79    80    100
+constexpr TileVariant kGatedVariants[] = {
+    {tile_id(64, 128), 64, 128, 3340, 350, 390, 601, 1260, 1.0},
+    {tile_id(128, 128), 128, 128, 950, 441, 530, 982, 3900, 1.0},
+    {tile_id(256, 128), 256, 128, 0, 713, 814, 1587, 6000, 1.0},
+    {tile_id(256, 256), 256, 256, 0, 1277, 1454, 2903, 7800, 1.0}};
+constexpr FewRowsCost kGatedFew = {1970, 1.26, 1.59, 14.3, 1.0};
+
+// Rows, 2F weight rows and K of a gated block on E4M3 operands to its kernel.
+inline int pick_gated(int64_t M, int64_t weight_rows, int64_t K, int cus) {
+  return pick_variant(kGatedVariants, kGatedFew, M, weight_rows, K, 128, cus);
+}
+
 }  // namespace fp8q
