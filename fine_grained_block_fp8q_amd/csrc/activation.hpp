@@ -70,8 +70,11 @@ __device__ __forceinline__ float act_f32(int act, float x) {
   return e < __builtin_inff() ? x * (s * 0x1p-16f) : 0.0f * x;
 }
 
-// act(x) and act'(x) to a few FP32 units: their results are quantized, and a
-// code changes where an error moves a value over a rounding boundary.  The
+// act(x) and act'(x): their results are quantized, and a code changes where an
+// error moves a value over a rounding boundary.  Over every BF16 gate act is
+// within 3 FP32 units for SiLU (0.8 on average to |x| = 8) and, by the rounding of
+// y, 110 for GELU (at -9; 1.7 on average); act' is within as many of its terms, so
+// near its zero within more of itself (272 at -1.28, 470 at -0.754).  The
 // exponential is the hardware's with its argument's rounding put right
 // (exp(-y) = 2^t, t = -y log2 e; r is what FP32 t lost, and 2^(t + r) =
 // 2^t (1 + r ln 2)), and the reciprocal gets one Newton step: 12 instructions,

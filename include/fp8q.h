@@ -379,6 +379,8 @@ fp8q_status fp8q_quantize_token_i8(const void* x_bf16, int64_t M, int64_t K, int
  * Accuracy: the integer sum is exact; it is converted to FP32 and scaled by
  * two FP32 products (and one addition), so
  *   |C - C_exact| <= 4 * 2^-24 * (|C_exact - bias| + |bias|)  (+ half a BF16 ulp).
+ * RANGE: the bound assumes that sum * a_s[m], formed first, and its product with
+ * w_s[n] are normal FP32 numbers or 0 (no overflow, nothing below 2^-126).
  */
 fp8q_status fp8q_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q, const float* w_s,
                          const float* bias, int64_t M, int64_t N, int64_t K, void* c,
@@ -392,7 +394,7 @@ fp8q_status fp8q_gemm_i8(const int8_t* a_q, const float* a_s, const int8_t* w_q,
  *   a_q : [M][K] int8, a_s : [M] float32;
  *   w_q : [2F][K] int8 (rows 0..F-1 gate, F..2F-1 up), w_s : [2F] float32
  *   h   : [M][F] float32 or bfloat16 (per `out`) (output).
- *   M >= 0, any F >= 0, K % 16 == 0; errors as fp8q_gemm_i8.
+ *   M >= 0, any F >= 0, K % 16 == 0; errors and RANGE as fp8q_gemm_i8.
  * act(x) = x sigma(y) (y = x, or 2 sqrt(2/pi) (x + 0.044715 x^3)) is evaluated
  * in FP32 with an error of at most 2^-128 |x| + 2^-149 and, relative to |act(x)|,
  * 8 * 2^-24 for FP32 output, (16 + 8|y|) 2^-24 for BF16 output.
@@ -404,8 +406,12 @@ fp8q_status fp8q_gemm_i8_gated(const int8_t* a_q, const float* a_s, const int8_t
 
 /*
  * Gated block on block-scaled E4M3 operands: with Y = fp8q_gemm's product of
- * the stacked gate and up weights (accuracy clause of fp8q_gemm),
+ * the stacked gate and up weights (accuracy and RANGE clauses of fp8q_gemm),
  *   h[m][f] = act(Y[m][f]) * Y[m][F + f].
+ * With many rows Y's sums are fp8q_gemm's bit for bit.  Few rows (always up to
+ * 16) take a kernel that adds a sum's chunks as 8 partial sums: within the same
+ * bound, but the last bits differ, so that a token's result depends on whether its
+ * call holds few rows or many.
  *   a_q : [M][K] uint8, a_s : [K/128][M] float32 (from fp8q_quantize_act)
  *   w_q : [2F][K] uint8 (rows 0..F-1 gate, F..2F-1 up), w_s : [2F/128][K/128]
  *         float32 (from fp8q_quantize_weight)
@@ -451,9 +457,15 @@ fp8q_status fp8q_grouped_gemm_gated(const uint8_t* a_q, const float* a_s, int64_
  *   dh      : [M][F] bfloat16; gate_up : [M][2F] bfloat16 (from fp8q_gemm_gated).
  *   M >= 0, F >= 0 with F % 128 == 0.
  * FP8Q_ERR_UNSUPPORTED: F > 2^22 (32-bit offsets within 128 tokens).
- * dY is not rounded before it is quantized; its FP32 values carry a relative
- * error of a few 2^-24, so a code can differ from that of the exact dY only
- * where the exact value lies that close to a rounding boundary.
+ * dY is not rounded before it is quantized.  With act(x) = x sigma(y), its FP32
+ * values are within
+ *   (16 + 8|y|) 2^-24 |dh| |up| (|act'(gate)| + |gate y' sigma(y) sigma(-y)|)  and
+ *   (16 + 8|y|) 2^-24 |dh| |act(gate)|
+ * of the exact dgate and dup (|y| counted up to 100, and 2^-119 beside it): the
+ * terms' size is what counts, so near the zero of act' dgate's error relative to
+ * itself is larger.  A code can differ from that of the exact dY where that lies
+ * within this error (its own, or of its group's largest value) of a rounding
+ * boundary.
  * RANGE: dY must stay below FLT_MAX.
  */
 fp8q_status fp8q_gated_backward(const void* dh, const void* gate_up, int64_t M, int64_t F,
