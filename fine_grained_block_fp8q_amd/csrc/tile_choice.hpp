@@ -33,8 +33,9 @@ struct FewRowsCost {
 // weight rows 64 to 8192, K 128 to 9000).  Against the best kernel of each
 // shape the choice costs 0.6% on average and 16% at most over 200 int8 shapes,
 // 0.2% and 15% over 138 E4M3 ones; over 40 of both that were not fitted, 1.6%
-// and 18%.  (With 17 to 32 rows it matters where weight rows make several rounds
-// of few-row workgroups: 32 x 32768 x 512 takes 10.4 us in those, 6.8 in tiles.)
+// and 18%.  From 17 to 32 rows, outside the fit (60 shapes of each, weight rows
+// to 65536): 0.3% and 11%, 0.1% and 2%; the kernel for few rows alone would cost
+// 5% and 94%, 6% and 88% (32 x 32768 x 512: 10.4 us, 6.8 in tiles).
 template <int N>
 inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few, int64_t M,
                         int64_t weight_rows, int64_t K, int step, int cus) {
@@ -65,7 +66,8 @@ inline int pick_variant(const TileVariant (&variants)[N], const FewRowsCost& few
   return best;
 }
 
-// int8 products (i8_tiles.hip): kernel times with 4096 weight rows, K = 7168, in us, by number of rows:
+// int8 products (i8_tiles.hip): kernel times with 4096 weight rows, K = 7168, in
+// us, by number of rows:
 //   rows          64    128   256   384   512   768   1024  2048  4096
 //   few rows      10.2  15.7  29
 //   32 x 64       14.2  14.3  18.3  31
@@ -89,8 +91,8 @@ inline int pick_i8(int64_t M, int64_t weight_rows, int64_t K, int cus) {
   return pick_variant(kI8Variants, kI8Few, M, weight_rows, K, 256, cus);
 }
 
-// The gated block on E4M3 operands (gated_gemm.hip): kernel times with F = 2048 (4096 weight rows), K = 7168, in us, by number of
-// rows:
+// The gated block on E4M3 operands (gated_gemm.hip): kernel times with F = 2048
+// (4096 weight rows), K = 7168, in us, by number of rows:
 //   rows          1     32    64    128   256   512   1024  2048  4096
 //   few rows      7.2   7.8   10.8  16.7  32
 //   64 x 128                  24.2  24.2  24.5  26    40    79    157
