@@ -81,7 +81,8 @@ __device__ __forceinline__ float act_f32(int act, float x) {
 // where the library's exponential and a correctly rounded division take 30 of
 // a kernel that they would bound (4000 tokens, F = 2048: 18.2 us for 16.6, with
 // 702 and 794 of 393 million codes off the exact formula's for SiLU and GELU where
-// these give 724 and 783: the scale's and the products' roundings decide).  From t = 126 on the sigmoid is taken as 0.
+// these give 724 and 783: the scale's and the products' roundings decide).  From
+// t = 126 on the sigmoid is taken as 0.
 __device__ __forceinline__ void act_and_grad(int act, float x, float& a, float& da) {
   // act'(x) is 1 or 0 beyond |x| = 1000, also of the clamped value; the clamp
   // keeps x^3 and the products below finite
