@@ -84,6 +84,44 @@ lib.fp8q_grouped_gemm_gated.argtypes = [_p, _p, _i64, _p, _i32, _p, _p, _i64, _i
 lib.fp8q_grouped_gemm_gated.restype = _st
 lib.fp8q_gated_backward.argtypes = [_p, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _p, _p]
 lib.fp8q_gated_backward.restype = _st
+_f32 = ctypes.c_float
+lib.fp8q_layer_norm.argtypes = [_p, _i32, _p, _p, _i64, _i64, _f32, _p, _i32, _p, _p, _i32, _p, _p,
+                                _p]
+lib.fp8q_layer_norm.restype = _st
+lib.fp8q_layer_norm_backward_workspace.argtypes = [_i64, _i64]
+lib.fp8q_layer_norm_backward_workspace.restype = _i64
+lib.fp8q_layer_norm_backward.argtypes = [_p, _i32, _p, _i32, _p, _p, _p, _i64, _i64, _p, _p, _p,
+                                         _p, _p]
+lib.fp8q_layer_norm_backward.restype = _st
+lib.fp8q_expert_columns.argtypes = [_i64, _i32]
+lib.fp8q_expert_columns.restype = _i64
+lib.fp8q_grouped_quantize_act_t.argtypes = [_p, _i64, _p, _i32, _i64, _p, _p, _i32, _p]
+lib.fp8q_grouped_quantize_act_t.restype = _st
+lib.fp8q_grouped_gated_backward.argtypes = [_p, _p, _i64, _p, _i32, _i64, _i32, _i32, _p, _p, _p,
+                                            _p, _p]
+lib.fp8q_grouped_gated_backward.restype = _st
+lib.fp8q_grouped_gemm_rowscaled.argtypes = [_p, _p, _p, _p, _i64, _p, _i32, _i64, _i64, _p, _i32,
+                                            _p]
+lib.fp8q_grouped_gemm_rowscaled.restype = _st
+lib.fp8q_grouped_gemm_rowscaled_precise.argtypes = lib.fp8q_grouped_gemm_rowscaled.argtypes
+lib.fp8q_grouped_gemm_rowscaled_precise.restype = _st
+
+
+class AdamwTensor(ctypes.Structure):
+    """fp8q_adamw_tensor"""
+    _fields_ = [("p", _p), ("g", _p), ("m", _p), ("v", _p), ("m_s", _p), ("v_s", _p), ("copy", _p),
+                ("n", _i64)]
+
+
+class AdamwArgs(ctypes.Structure):
+    """fp8q_adamw_args"""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+               [("step", _i64), ("lr_dev", _p), ("step_dev", _p), ("grad_scale", _p)]
+
+
+lib.fp8q_adamw.argtypes = [ctypes.POINTER(AdamwTensor), _i32, ctypes.POINTER(AdamwArgs), _i32, _i32,
+                           _p]
+lib.fp8q_adamw.restype = _st
 lib.fp8q_status_string.argtypes = [_st]
 lib.fp8q_status_string.restype = ctypes.c_char_p
 lib.fp8q_abi_version.argtypes = []
@@ -97,6 +135,7 @@ lib.fp8q_debug_checks.restype = ctypes.c_int
 SCALE_F32, SCALE_POW2 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 ACT_SILU, ACT_GELU_TANH = 0, 1
+MOMENTS_F32, MOMENTS_E4M3 = 0, 1
 GROUP = 128
 
 _MODES = {"f32": SCALE_F32, "pow2": SCALE_POW2, SCALE_F32: SCALE_F32, SCALE_POW2: SCALE_POW2}
@@ -565,6 +604,266 @@ def fp8q_gated_backward(dh, gate_up, q, s, qt, st, act="silu", mode="f32", strea
                                       _stream(stream, dev)), wh)
 
 
+def _positive_rows(where, N):
+    if not 1 <= N <= 16384:
+        raise ValueError(f"{where}: rows of {N} elements, expected 1 to 16384")
+
+
+def _type_code(where, name, t):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{where}: {name} must be a torch.Tensor")
+    code = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{where}: {name} has dtype {t.dtype}, expected float32 or bfloat16")
+    return code
+
+
+def fp8q_layer_norm(x, weight, bias, mean, rstd, y=None, q=None, s=None, eps=1e-5, mode="f32",
+                    stream=None):
+    """y = (x - mean) * rstd * weight (+ bias) of the rows of x (float32 or
+    bfloat16 [M][N]; weight and bias float32 [N], bias may be None), into y
+    (float32 or bfloat16 [M][N]), into q (uint8 [M][N]) and s (float32
+    [N/128][M]) as E4M3, or into both; mean and rstd (float32 [M]) are written."""
+    import torch
+    wh = "fp8q_layer_norm"
+    M, N = _dims(wh, x, 2, "x")
+    _positive_rows(wh, N)
+    dev = x.device
+    xt = _type_code(wh, "x", x)
+    _need(wh, dev, ("x", x, x.dtype, (M, N)), ("weight", weight, torch.float32, (N,)),
+          ("mean", mean, torch.float32, (M,)), ("rstd", rstd, torch.float32, (M,)))
+    if bias is not None:
+        _need(wh, dev, ("bias", bias, torch.float32, (N,)))
+    if (q is None) != (s is None) or (q is None and y is None):
+        raise ValueError(f"{wh}: codes and scales come in a pair, and y or they are wanted")
+    yt = OUT_F32
+    if y is not None:
+        _req(wh, "y", y, ["f32", "bf16"], (M, N), dev)
+        yt = _type_code(wh, "y", y)
+    if q is not None:
+        _mult128(wh, N=N)
+        _need(wh, dev, ("q", q, torch.uint8, (M, N)), ("s", s, torch.float32, (N // GROUP, M)))
+    _invoke(lib.fp8q_layer_norm, (x.data_ptr(), xt, weight.data_ptr(), _at(bias), M, N, eps, _at(y),
+                                  yt, _at(q), _at(s), _MODES[mode], mean.data_ptr(),
+                                  rstd.data_ptr(), _stream(stream, dev)), wh)
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+def layer_norm_backward_workspace(M, N):
+    """Bytes of workspace that fp8q_layer_norm_backward takes."""
+    return lib.fp8q_layer_norm_backward_workspace(M, N)
+
+
+def fp8q_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream=None):
+    """dx (of x's type) and the sums over all rows dweight and dbias (float32
+    [N]; dbias may be None) from dy (float32 or bfloat16 [M][N]) and what
+    fp8q_layer_norm read and wrote; workspace: uint8
+    [layer_norm_backward_workspace(M, N)]."""
+    import torch
+    wh = "fp8q_layer_norm_backward"
+    M, N = _dims(wh, x, 2, "x")
+    _positive_rows(wh, N)
+    dev = x.device
+    xt = _type_code(wh, "x", x)
+    _req(wh, "dy", dy, ["f32", "bf16"], (M, N), dev)
+    _need(wh, dev, ("x", x, x.dtype, (M, N)), ("weight", weight, torch.float32, (N,)),
+          ("mean", mean, torch.float32, (M,)), ("rstd", rstd, torch.float32, (M,)),
+          ("dx", dx, x.dtype, (M, N)), ("dweight", dweight, torch.float32, (N,)),
+          ("workspace", workspace, torch.uint8, (layer_norm_backward_workspace(M, N),)))
+    if dbias is not None:
+        _need(wh, dev, ("dbias", dbias, torch.float32, (N,)))
+    _invoke(lib.fp8q_layer_norm_backward,
+            (dy.data_ptr(), _type_code(wh, "dy", dy), x.data_ptr(), xt, weight.data_ptr(),
+             mean.data_ptr(), rstd.data_ptr(), M, N, dx.data_ptr(), dweight.data_ptr(), _at(dbias),
+             workspace.data_ptr(), _stream(stream, dev)), wh)
+
+
+def expert_columns(M_total, G):
+    """Columns of an operand whose M_total tokens are grouped by G experts, in
+    groups of 128 that hold one expert's tokens each."""
+    return lib.fp8q_expert_columns(M_total, G)
+
+
+def _offsets(where, off, dev):
+    import torch
+    (n,) = _dims(where, off, 1, "off")
+    if n < 2:
+        raise ValueError(f"{where}: off has {n} elements, expected G + 1 of 1 expert at least")
+    _need(where, dev, ("off", off, torch.int32, (n,)))
+    return n - 1
+
+
+def fp8q_grouped_quantize_act_t(x, off, q_t, s_t, mode="f32", stream=None):
+    """x: bf16 [M_total][K], rows [off[e], off[e+1]) of expert e -> q_t: uint8
+    [K][T], s_t: float32 [T/128][K], T = expert_columns(M_total, G) (in place)."""
+    import torch
+    wh = "fp8q_grouped_quantize_act_t"
+    M, K = _dims(wh, x, 2, "x")
+    _mult128(wh, K=K)
+    dev = x.device
+    G = _offsets(wh, off, dev)
+    T = expert_columns(M, G)
+    _need(wh, dev, ("x", x, torch.bfloat16, (M, K)), ("q_t", q_t, torch.uint8, (K, T)),
+          ("s_t", s_t, torch.float32, (T // GROUP, K)))
+    _invoke(lib.fp8q_grouped_quantize_act_t,
+            (x.data_ptr(), M, off.data_ptr(), G, K, q_t.data_ptr(), s_t.data_ptr(), _MODES[mode],
+             _stream(stream, dev)), wh)
+
+
+def fp8q_grouped_gated_backward(dh, gate_up, off, q, s, qt, st, act="silu", mode="f32",
+                                stream=None):
+    """fp8q_gated_backward for routed experts: the groups of tokens of qt (uint8
+    [2F][T]) and st (float32 [T/128][2F]) hold one expert's tokens each, T =
+    expert_columns(M_total, G); rows of q and s past off[G] are not written."""
+    import torch
+    wh = "fp8q_grouped_gated_backward"
+    M, F = _dims(wh, dh, 2, "dh")
+    _mult128(wh, F=F)
+    dev = dh.device
+    G = _offsets(wh, off, dev)
+    _need(wh, dev, ("dh", dh, torch.bfloat16, (M, F)),
+          ("gate_up", gate_up, torch.bfloat16, (M, 2 * F)))
+    if (q is None) != (s is None) or (qt is None) != (st is None) or (q is None and qt is None):
+        raise ValueError(f"{wh}: codes and scales come in pairs, and one pair at least")
+    if q is not None:
+        _need(wh, dev, ("q", q, torch.uint8, (M, 2 * F)),
+              ("s", s, torch.float32, (2 * F // GROUP, M)))
+    if qt is not None:
+        T = expert_columns(M, G)
+        _need(wh, dev, ("qt", qt, torch.uint8, (2 * F, T)),
+              ("st", st, torch.float32, (T // GROUP, 2 * F)))
+    _invoke(lib.fp8q_grouped_gated_backward,
+            (dh.data_ptr(), gate_up.data_ptr(), M, off.data_ptr(), G, F, _act(wh, act),
+             _MODES[mode], _at(q), _at(s), _at(qt), _at(st), _stream(stream, dev)), wh)
+
+
+def _grouped_rowscaled(wh, cfunc, a_q, a_s, b_q, b_s, off, c, stream):
+    import torch
+    N, T = _dims(wh, a_q, 2, "a_q")
+    K, _ = _dims(wh, b_q, 2, "b_q")
+    _mult128(wh, N=N, K=K, T=T)
+    dev = a_q.device
+    G = _offsets(wh, off, dev)
+    _need(wh, dev, ("a_q", a_q, torch.uint8, (N, T)), ("a_s", a_s, torch.float32, (T // GROUP, N)),
+          ("b_q", b_q, torch.uint8, (K, T)), ("b_s", b_s, torch.float32, (T // GROUP, K)))
+    _req(wh, "c", c, ["f32", "bf16"], (G, N, K), dev)
+    _invoke(cfunc, (a_q.data_ptr(), a_s.data_ptr(), b_q.data_ptr(), b_s.data_ptr(), T,
+                    off.data_ptr(), G, N, K, c.data_ptr(), _out_code(wh, c),
+                    _stream(stream, dev)), wh)
+
+
+def fp8q_grouped_gemm_rowscaled(a_q, a_s, b_q, b_s, off, c, stream=None):
+    """c[G][N][K] (float32 or bfloat16): of each expert its a_q [N][T] x b_q [K][T]^T
+    over its groups of tokens, 1x128 row-group scales on both (the weight
+    gradients dY^T X); off: the device int32[G+1] that grouped the tokens."""
+    _grouped_rowscaled("fp8q_grouped_gemm_rowscaled", lib.fp8q_grouped_gemm_rowscaled, a_q, a_s,
+                       b_q, b_s, off, c, stream)
+
+
+def fp8q_grouped_gemm_rowscaled_precise(a_q, a_s, b_q, b_s, off, c, stream=None):
+    """fp8q_grouped_gemm_rowscaled in the precise mode (FP16 MFMAs on the widened codes)."""
+    _grouped_rowscaled("fp8q_grouped_gemm_rowscaled_precise",
+                       lib.fp8q_grouped_gemm_rowscaled_precise, a_q, a_s, b_q, b_s, off, c, stream)
+
+
+def _scalar(where, name, t, dtype, dev):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.numel() != 1:
+        raise ValueError(f"{where}: {name} must be a torch.Tensor of one element")
+    _need(where, dev, (name, t, dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _adamw_args(where, step, lr, betas, eps, weight_decay, grad_scale, dev):
+    import torch
+    a = AdamwArgs()
+    if isinstance(lr, torch.Tensor):
+        a.lr_dev = _scalar(where, "lr", lr, torch.float32, dev)
+    else:
+        a.lr = lr
+    if isinstance(step, torch.Tensor):
+        a.step_dev = _scalar(where, "step", step, torch.int32, dev)
+    else:
+        a.step = step
+    if grad_scale is not None:
+        a.grad_scale = _scalar(where, "grad_scale", grad_scale, torch.float32, dev)
+    a.beta1, a.beta2 = betas
+    a.eps, a.weight_decay = eps, weight_decay
+    values = [(n, getattr(a, n)) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")]
+    for n, v in values:
+        if not 0 <= v < (1 if n.startswith("beta") else float("inf")):
+            raise ValueError(f"{where}: {n} = {v}")
+    if not a.step_dev and a.step < 1:
+        raise ValueError(f"{where}: step = {step}, the first is 1")
+    return a
+
+
+def _bumped(tensors):
+    """Tells autograd that these were written."""
+    import torch
+    for t in tensors:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
+def _adamw_call(where, params, grads, m, m_s, v, v_s, step, lr, betas, eps, weight_decay,
+                grad_scale, copies, stream):
+    import torch
+    n = len(params)
+    lists = {"grads": grads, "exp_avgs": m, "exp_avg_sqs": v, "exp_avg_scales": m_s,
+             "exp_avg_sq_scales": v_s, "copies": copies}
+    for name, l in lists.items():
+        if l is not None and len(l) != n:
+            raise ValueError(f"{where}: {n} params, {len(l)} {name}")
+    if n == 0:
+        return
+    if not isinstance(params[0], torch.Tensor):
+        raise ValueError(f"{where}: params must be torch.Tensors")
+    dev = params[0].device
+    eight = m_s is not None
+    grad_type = _type_code(where, "grads[0]", grads[0])
+    moment = torch.uint8 if eight else torch.float32
+    array = (AdamwTensor * n)()
+    for i, (p, a) in enumerate(zip(params, array)):
+        if not isinstance(p, torch.Tensor):
+            raise ValueError(f"{where}: params[{i}] must be a torch.Tensor")
+        shape, count = tuple(p.shape), p.numel()
+        _need(where, dev, (f"params[{i}]", p, torch.float32, shape),
+              (f"grads[{i}]", grads[i], grads[0].dtype, shape),
+              (f"exp_avgs[{i}]", m[i], moment, shape), (f"exp_avg_sqs[{i}]", v[i], moment, shape))
+        a.p, a.g, a.m, a.v, a.n = p.data_ptr(), grads[i].data_ptr(), m[i].data_ptr(), \
+            v[i].data_ptr(), count
+        if eight:
+            groups = (-(-count // GROUP),)
+            _need(where, dev, (f"exp_avg_scales[{i}]", m_s[i], torch.float32, groups),
+                  (f"exp_avg_sq_scales[{i}]", v_s[i], torch.float32, groups))
+            a.m_s, a.v_s = m_s[i].data_ptr(), v_s[i].data_ptr()
+        if copies is not None:
+            _need(where, dev, (f"copies[{i}]", copies[i], torch.bfloat16, shape))
+            a.copy = copies[i].data_ptr()
+    args = _adamw_args(where, step, lr, betas, eps, weight_decay, grad_scale, dev)
+    _invoke(lib.fp8q_adamw, (array, n, args, grad_type, MOMENTS_E4M3 if eight else MOMENTS_F32,
+                             _stream(stream, dev)), where)
+    for l in (params, m, v, m_s, v_s, copies):
+        if l is not None:
+            _bumped(l)
+
+
+def fp8q_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.95), eps=1e-8,
+               weight_decay=0.1, exp_avg_scales=None, exp_avg_sq_scales=None, grad_scale=None,
+               copies=None, stream=None):
+    """One AdamW step over lists of tensors, in place: see adamw and adamw_8bit
+    (which have the scales)."""
+    if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
+        raise ValueError("fp8q_adamw: both moments have scales, or neither")
+    _adamw_call("fp8q_adamw", params, grads, exp_avgs, exp_avg_scales, exp_avg_sqs,
+                exp_avg_sq_scales, step, lr, betas, eps, weight_decay, grad_scale, copies, stream)
+
+
 # ---------------------------------------------------------- allocation helpers
 def quantize_act(x, mode="f32", stream=None):
     import torch
@@ -657,6 +956,8 @@ class _PythonPath:
         return None
 
     quantize_token_i8 = gemm_i8 = gemm_i8_gated = gemm_gated = gated_backward = _decline
+    layer_norm = layer_norm_backward = grouped_quantize_act_t = _decline
+    grouped_gated_backward = grouped_gemm_rowscaled = adamw = _decline
 
 
 def _compiled():
@@ -676,7 +977,10 @@ def _compiled():
         return _native
     _calls.entries(*(ctypes.cast(getattr(lib, "fp8q_" + n), _p).value for n in
                      ("quantize_token_i8", "gemm_i8", "gemm_i8_gated", "gemm_gated",
-                      "grouped_gemm_gated", "gated_backward")))
+                      "grouped_gemm_gated", "gated_backward", "layer_norm",
+                      "layer_norm_backward_workspace", "layer_norm_backward", "expert_columns",
+                      "grouped_quantize_act_t", "grouped_gated_backward",
+                      "grouped_gemm_rowscaled", "grouped_gemm_rowscaled_precise", "adamw")))
     _native = _calls
     return _native
 
@@ -790,3 +1094,163 @@ def gated_backward(dh, gate_up, act="silu", mode="f32", rows=True, tokens=True, 
         st = torch.empty((groups, 2 * F), dtype=torch.float32, device=dev)
     fp8q_gated_backward(dh, gate_up, q, s, qt, st, act, mode, stream)
     return q, s, qt, st
+
+
+def _norm(wh, x, weight, bias, eps, out_dtype, want_y, codes, mode, stream):
+    if stream is None:
+        native = _native or _compiled()
+        out = (OUT_BF16 if out_dtype is None else _OUT_OF.get(out_dtype)) if want_y else -1
+        if out is not None:
+            r = native.layer_norm(x, weight, bias, eps, out, codes, _MODES[mode])
+            if r is not None:
+                return r if type(r) is not int else _refused(r, wh)
+    import torch
+    M, N = _dims(wh, x, 2, "x")
+    _positive_rows(wh, N)
+    if codes:
+        _mult128(wh, N=N)
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)   # noqa: E731
+    y = new((M, N), out_dtype or torch.bfloat16) if want_y else None
+    q = new((M, N), torch.uint8) if codes else None
+    s = new((N // GROUP, M), torch.float32) if codes else None
+    mean, rstd = new((M,), torch.float32), new((M,), torch.float32)
+    fp8q_layer_norm(x, weight, bias, mean, rstd, y, q, s, eps, mode, stream)
+    return y, q, s, mean, rstd
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, out_dtype=None, stream=None):
+    """(y, mean, rstd): layer norm of the rows of x (float32 or bfloat16 [M][N],
+    weight and bias float32 [N]); y is bfloat16 unless out_dtype says float32."""
+    y, _, _, mean, rstd = _norm("fp8q_layer_norm", x, weight, bias, eps, out_dtype, True, False,
+                                "f32", stream)
+    return y, mean, rstd
+
+
+def layer_norm_quantized(x, weight, bias=None, eps=1e-5, mode="f32", save_y=False, out_dtype=None,
+                         stream=None):
+    """(q, s, mean, rstd): layer norm written as the E4M3 operand of gemm, from y
+    in float32; with save_y, (q, s, mean, rstd, y), y as layer_norm's."""
+    y, q, s, mean, rstd = _norm("fp8q_layer_norm", x, weight, bias, eps, out_dtype, save_y, True,
+                                mode, stream)
+    return (q, s, mean, rstd, y) if save_y else (q, s, mean, rstd)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, stream=None):
+    """(dx, dweight, dbias): the gradients of layer_norm, dx of x's type, the
+    others float32; bias=False leaves dbias out (None)."""
+    wh = "fp8q_layer_norm_backward"
+    if stream is None:
+        r = (_native or _compiled()).layer_norm_backward(dy, x, weight, mean, rstd, bias)
+        if r is not None:
+            return r if type(r) is not int else _refused(r, wh)
+    import torch
+    M, N = _dims(wh, x, 2, "x")
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    new = lambda n, dt: torch.empty((n,), dtype=dt, device=x.device)   # noqa: E731
+    dweight = new(N, torch.float32)
+    dbias = new(N, torch.float32) if bias else None
+    work = new(layer_norm_backward_workspace(M, N), torch.uint8)
+    fp8q_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, work, stream)
+    return dx, dweight, dbias
+
+
+def grouped_quantize_act_t(x, off, mode="f32", stream=None):
+    """(q_t, s_t): x (bf16 [M_total][K], rows grouped by expert) in E4M3 along the
+    tokens, for grouped_gemm_rowscaled: uint8 [K][T] and float32 [T/128][K], T =
+    expert_columns(M_total, G)."""
+    wh = "fp8q_grouped_quantize_act_t"
+    if stream is None:
+        r = (_native or _compiled()).grouped_quantize_act_t(x, off, _MODES[mode])
+        if r is not None:
+            return r if type(r) is not int else _refused(r, wh)
+    import torch
+    M, K = _dims(wh, x, 2, "x")
+    T = expert_columns(M, _offsets(wh, off, x.device))
+    q = torch.empty((K, T), dtype=torch.uint8, device=x.device)
+    s = torch.empty((T // GROUP, K), dtype=torch.float32, device=x.device)
+    fp8q_grouped_quantize_act_t(x, off, q, s, mode, stream)
+    return q, s
+
+
+def grouped_gated_backward(dh, gate_up, off, act="silu", mode="f32", rows=True, tokens=True,
+                           stream=None):
+    """(q, s, qt, st): gated_backward by expert, for grouped_gemm (dX) and
+    grouped_gemm_rowscaled (dW); rows of q and s past off[G] are not written."""
+    wh = "fp8q_grouped_gated_backward"
+    if stream is None:
+        r = (_native or _compiled()).grouped_gated_backward(dh, gate_up, off, _act(wh, act),
+                                                            _MODES[mode], rows, tokens)
+        if r is not None:
+            return r if type(r) is not int else _refused(r, wh)
+    import torch
+    M, F = _dims(wh, dh, 2, "dh")
+    dev = dh.device
+    T = expert_columns(M, _offsets(wh, off, dev))
+    q = s = qt = st = None
+    if rows:
+        q = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
+        s = torch.empty((2 * F // GROUP, M), dtype=torch.float32, device=dev)
+    if tokens:
+        qt = torch.empty((2 * F, T), dtype=torch.uint8, device=dev)
+        st = torch.empty((T // GROUP, 2 * F), dtype=torch.float32, device=dev)
+    fp8q_grouped_gated_backward(dh, gate_up, off, q, s, qt, st, act, mode, stream)
+    return q, s, qt, st
+
+
+def grouped_gemm_rowscaled(a_q, a_s, b_q, b_s, off, out_dtype=None, stream=None, precise=False):
+    """[G][N][K]: the weight gradients of all experts from both operands' codes
+    along the tokens (grouped_quantize_act_t, grouped_gated_backward); zeros for
+    an expert without tokens."""
+    wh = "fp8q_grouped_gemm_rowscaled" + ("_precise" if precise else "")
+    if stream is None:
+        native = _native or _compiled()
+        out = OUT_F32 if out_dtype is None else _OUT_OF.get(out_dtype)
+        if out is not None:
+            r = native.grouped_gemm_rowscaled(a_q, a_s, b_q, b_s, off, out, precise)
+            if r is not None:
+                return r if type(r) is not int else _refused(r, wh)
+    import torch
+    N, K = _rows(wh, a_q, b_q)
+    G = _offsets(wh, off, a_q.device)
+    c = torch.empty((G, N, K), dtype=out_dtype or torch.float32, device=a_q.device)
+    f = fp8q_grouped_gemm_rowscaled_precise if precise else fp8q_grouped_gemm_rowscaled
+    f(a_q, a_s, b_q, b_s, off, c, stream)
+    return c
+
+
+def _adamw(params, grads, m, m_s, v, v_s, step, lr, betas, eps, weight_decay, grad_scale, copies,
+           stream):
+    wh = "fp8q_adamw"
+    if stream is None:
+        r = (_native or _compiled()).adamw(params, grads, m, m_s, v, v_s, copies, step, lr, *betas,
+                                           eps, weight_decay, grad_scale)
+        if r is not None:
+            return None if r == OK else _refused(r, wh)
+    _adamw_call(wh, params, grads, m, m_s, v, v_s, step, lr, betas, eps, weight_decay, grad_scale,
+                copies, stream)
+
+
+def adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.95), eps=1e-8,
+          weight_decay=0.1, grad_scale=None, copies=None, stream=None):
+    """One AdamW step over lists of tensors, in place.  params (masters) and both
+    moments are float32, grads float32 or bfloat16 (one type), each of its
+    parameter's shape; copies, if given, take the new parameters as bfloat16.
+    step counts from 1.  step and lr may be device tensors of one element (int32
+    and float32), which a captured graph reads at each replay; grad_scale
+    (float32, on the device) multiplies the gradients."""
+    _adamw(params, grads, exp_avgs, None, exp_avg_sqs, None, step, lr, betas, eps, weight_decay,
+           grad_scale, copies, stream)
+
+
+def adamw_8bit(params, grads, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, step,
+               lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, grad_scale=None,
+               copies=None, stream=None):
+    """adamw with both moments in E4M3: exp_avgs holds the codes (uint8, the
+    parameter's shape) of the first moment, exp_avg_sqs those of the second
+    moment's square root, 128 consecutive elements with one scale (float32
+    [ceil(n/128)]).  Zero codes and scales are the state before the first step.
+    The codes are rounded with a dither of the element's place and the step, so
+    that a moment which moves by less than a code's step each time does not stay
+    where it is."""
+    _adamw(params, grads, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, step, lr,
+           betas, eps, weight_decay, grad_scale, copies, stream)

@@ -54,6 +54,11 @@ SOURCES = {
     "few_rows.hip": [],
     "i8_tiles.hip": [],
     "gated_backward.hip": [],
+    "layer_norm.hip": [],
+    "expert_tokens.hip": [],
+    "grouped_rowscaled.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    # the moments' codes are a bit-exact contract
+    "adamw.hip": ["-ffp-contract=off"],
     "fp8q_api.hip": [],
 }
 

@@ -1,0 +1,309 @@
+// One AdamW step over many tensors.
+//
+// Per element, with t the step's number and g the gradient (times grad_scale):
+//   m' = fl(fl(b1 m) + fl((1 - b1) g)),  v' = fl(fl(b2 v) + fl((1 - b2) fl(g g))),
+//   p' = p (1 - lr wd) - lr/(1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps),
+// masters in FP32, moments in FP32 or in 8 bits.  Bound by memory: a master is
+// read and written (8 bytes), the gradient read (2 or 4), the moments read and
+// written (16, or 4 and the scales), the BF16 copy written (2).
+//
+// Moments in 8 bits: E4M3 codes of m' and of sqrt(v') (the root has half the
+// exponent range of v', so 128 elements of one scale reach 2^35 down from the
+// largest v'), 128 consecutive elements a scale: amax fl(1/448), the codes those of
+// the values times 448 fl(1/amax) (one division a group).  The codes are not rounded to the nearest: a moment moves by a small part of itself
+// a step (5% of v' at b2 = 0.95, 2.5% of its root), less than half of E4M3's
+// step, and would never leave its code.  Each magnitude x is rounded up where
+// its fraction of a step and a dither u reach 1, u = frac(t phi + i psi) in 20
+// bits with i the element's place in its tensor: over the steps of one element
+// the u are spread evenly, so that the codes of a value that stands have its mean.
+// (A moment feeds back into the next step, whose u is related: under a constant
+// gradient the codes' mean is off by 0.3% on average and 1.4% at most, against 0
+// and 1.6% of independent u.)  A root that is not zero keeps a code that is not
+// zero: m' is never divided by eps alone.
+//
+// A workgroup of 256 lanes takes 2048 consecutive elements of one tensor, 16
+// lanes (a DPP row) a group: lane l16 holds elements 4 l16 .. +3 and 64 + 4 l16
+// .. +3 of its group, so that 16 lanes' loads of FP32 are 256 consecutive bytes.
+// Up to kTensors tensors go out in one launch, described in its arguments; a
+// workgroup finds its tensor from the tensors' first workgroups, one a lane.
+
+#include <math.h>
+
+#include "fp8q.h"
+#include "launch.hpp"
+#include "fp8q_device.hpp"
+
+namespace fp8q {
+
+constexpr int kThreads = 256;
+constexpr int kElems = 2048;   // of one workgroup
+constexpr int kTensors = 48;   // of one launch: what 4 KiB of arguments hold
+
+struct AdamwLaunch {
+  fp8q_adamw_tensor t[kTensors];
+  int32_t first[64];  // first workgroup of each tensor; past the last, INT32_MAX
+  const float* lr;    // on the device, or NULL
+  const int32_t* step;
+  const float* grad_scale;
+  double log_b1, log_b2, lr_host, decay;
+  float b1, one_b1, b2, one_b2, eps;
+  float keep, rate, inv_root;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  uint32_t dither;             // t's part of the dither
+};
+
+constexpr uint32_t kDitherStep = 0x9E3779B1u, kDitherPlace = 0x85EBCA6Bu;
+
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+// |x| <= 448 (1 + 2^-23) rounded to E4M3 with the dither's 20 bits u: the step of
+// E4M3 is the 20th bit of an FP32 value; below 2^-6, of the value 2^-6 higher.
+__device__ __forceinline__ float dithered(float x, uint32_t u) {
+  const bool sub = x < 0x1p-6f;
+  const float y = sub ? x + 0x1p-6f : x;
+  const float r = __uint_as_float((__float_as_uint(y) + u) & ~0xFFFFFu);
+  return fminf(sub ? r - 0x1p-6f : r, kE4M3Max);
+}
+
+// Scale and multiplier of a group of moments, 0 where the multiplier is not finite.
+struct MomentRule {
+  float mul, s;
+};
+__device__ __forceinline__ MomentRule moment_rule(float amax) {
+  const float mul = kE4M3Max * (1.f / amax);
+  const bool flushed = !__builtin_isfinite(mul);
+  return {flushed ? 0.f : mul, flushed ? 0.f : amax * (1.f / kE4M3Max)};
+}
+
+template <bool BF16_GRAD>
+__device__ __forceinline__ v4f load_grad(const void* g, int64_t i) {
+  if constexpr (BF16_GRAD) {
+    const v2u w = *reinterpret_cast<const v2u*>(static_cast<const uint16_t*>(g) + i);
+    return v4f{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+  } else {
+    return *reinterpret_cast<const v4f*>(static_cast<const float*>(g) + i);
+  }
+}
+
+template <bool BF16_GRAD>
+__device__ __forceinline__ float load_grad1(const void* g, int64_t i) {
+  if constexpr (BF16_GRAD)
+    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[i] << 16);
+  else
+    return static_cast<const float*>(g)[i];
+}
+
+__device__ __forceinline__ v4f unpack_e4m3x4(uint32_t w) {
+  return v4f{__builtin_amdgcn_cvt_f32_fp8((int)w, 0), __builtin_amdgcn_cvt_f32_fp8((int)w, 1),
+             __builtin_amdgcn_cvt_f32_fp8((int)w, 2), __builtin_amdgcn_cvt_f32_fp8((int)w, 3)};
+}
+
+// The first `n` (1 .. 4) elements from at; the others 0.
+template <class F>
+__device__ __forceinline__ v4f some(int n, F at) {
+  v4f r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < n) r[j] = at(j);
+  return r;
+}
+
+template <bool E4M3_MOMENTS, bool BF16_GRAD>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch a) {
+  const int lane = threadIdx.x & 63;
+  const int bid = (int)blockIdx.x;
+  const uint64_t upto = __ballot(a.first[lane] <= bid);
+  const int ti = __builtin_amdgcn_readfirstlane(__builtin_popcountll(upto) - 1);
+  const fp8q_adamw_tensor t = a.t[ti];
+  const int64_t base = (int64_t)(bid - a.first[ti]) * kElems;
+  const int64_t n = t.n;
+
+  float keep = a.keep, rate = a.rate, inv_root = a.inv_root;
+  uint32_t step_dither = a.dither;
+  if (a.step || a.lr) {
+    const double lr = a.lr ? (double)*a.lr : a.lr_host;
+    keep = (float)(1.0 - lr * a.decay);
+    if (a.step) {
+      const int32_t st = *a.step;
+      rate = (float)(lr / -expm1((double)st * a.log_b1));
+      inv_root = (float)(1.0 / sqrt(-expm1((double)st * a.log_b2)));
+      step_dither = (uint32_t)st * kDitherStep;
+    } else {
+      rate = (float)(lr * (double)a.rate);  // a.rate: 1 / (1 - b1^t)
+    }
+  }
+  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+
+  const int l16 = lane & 15;
+  const int64_t group = base + (int64_t)(threadIdx.x >> 4) * kGroup;
+  if (group >= n) return;  // (whole DPP rows)
+  int64_t at[2];
+  int live[2];
+  v4f p[2], g[2], m[2], v[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    at[h] = group + 64 * h + 4 * l16;
+    const int64_t rest = n - at[h];
+    live[h] = rest >= 4 ? 4 : rest > 0 ? (int)rest : 0;
+    const int64_t i = at[h];
+    if (live[h] == 4) {
+      p[h] = *reinterpret_cast<const v4f*>(t.p + i);
+      g[h] = load_grad<BF16_GRAD>(t.g, i);
+      if constexpr (E4M3_MOMENTS) {
+        m[h] = unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(t.m) + i));
+        v[h] = unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(t.v) + i));
+      } else {
+        m[h] = *reinterpret_cast<const v4f*>(static_cast<float*>(t.m) + i);
+        v[h] = *reinterpret_cast<const v4f*>(static_cast<float*>(t.v) + i);
+      }
+    } else {
+      const int c = live[h];
+      p[h] = some(c, [&](int j) { return t.p[i + j]; });
+      g[h] = some(c, [&](int j) { return load_grad1<BF16_GRAD>(t.g, i + j); });
+      if constexpr (E4M3_MOMENTS) {
+        auto one = [&](void* b, int j) {
+          return __builtin_amdgcn_cvt_f32_fp8((int)static_cast<uint8_t*>(b)[i + j], 0);
+        };
+        m[h] = some(c, [&](int j) { return one(t.m, j); });
+        v[h] = some(c, [&](int j) { return one(t.v, j); });
+      } else {
+        m[h] = some(c, [&](int j) { return static_cast<float*>(t.m)[i + j]; });
+        v[h] = some(c, [&](int j) { return static_cast<float*>(t.v)[i + j]; });
+      }
+    }
+  }
+  float ms = 1.f, vs = 1.f;
+  if constexpr (E4M3_MOMENTS) {
+    ms = t.m_s[group / kGroup];
+    vs = t.v_s[group / kGroup];
+  }
+
+  v4f root[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = g[h][j] * gs;
+      float m0 = m[h][j], v0 = v[h][j];
+      if constexpr (E4M3_MOMENTS) {
+        m0 = m0 * ms;
+        const float r = v0 * vs;
+        v0 = r * r;
+      }
+      m[h][j] = m0 * a.b1 + x * a.one_b1;
+      v[h][j] = v0 * a.b2 + (x * x) * a.one_b2;
+      root[h][j] = __builtin_sqrtf(v[h][j]);
+      const float den = __builtin_fmaf(root[h][j], inv_root, a.eps);
+      p[h][j] = __builtin_fmaf(p[h][j], keep, -((rate * m[h][j]) / den));
+    }
+
+  uint32_t mq[2], vq[2];
+  if constexpr (E4M3_MOMENTS) {
+    float am = 0.f, av = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        am = fmaxf(am, fabsf(m[h][j]));
+        av = fmaxf(av, root[h][j]);
+      }
+    const MomentRule rm = moment_rule(row16_max(am)), rv = moment_rule(row16_max(av));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v4f cm, cv;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t u = ((uint32_t)(at[h] + j) * kDitherPlace + step_dither) >> 12;
+        const float x = m[h][j] * rm.mul, y = root[h][j] * rv.mul;
+        cm[j] = copysignf(dithered(fabsf(x), u), x);
+        const float d = dithered(y, 0xFFFFFu - u);
+        cv[j] = d == 0.f && y > 0.f ? 0x1p-9f : d;
+      }
+      mq[h] = pack_e4m3x4(cm[0], cm[1], cm[2], cm[3]);
+      vq[h] = pack_e4m3x4(cv[0], cv[1], cv[2], cv[3]);
+    }
+    if (l16 == 0) {
+      t.m_s[group / kGroup] = rm.s;
+      t.v_s[group / kGroup] = rv.s;
+    }
+  }
+
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t i = at[h];
+    if (live[h] == 4) {
+      *reinterpret_cast<v4f*>(t.p + i) = p[h];
+      if constexpr (E4M3_MOMENTS) {
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i) = mq[h];
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i) = vq[h];
+      } else {
+        *reinterpret_cast<v4f*>(static_cast<float*>(t.m) + i) = m[h];
+        *reinterpret_cast<v4f*>(static_cast<float*>(t.v) + i) = v[h];
+      }
+      if (t.copy)
+        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(t.copy) + i) =
+            v2u{f32_to_bf16_bits(p[h][0]) | (f32_to_bf16_bits(p[h][1]) << 16),
+                f32_to_bf16_bits(p[h][2]) | (f32_to_bf16_bits(p[h][3]) << 16)};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= live[h]) continue;
+        t.p[i + j] = p[h][j];
+        if constexpr (E4M3_MOMENTS) {
+          static_cast<uint8_t*>(t.m)[i + j] = (uint8_t)(mq[h] >> (8 * j));
+          static_cast<uint8_t*>(t.v)[i + j] = (uint8_t)(vq[h] >> (8 * j));
+        } else {
+          static_cast<float*>(t.m)[i + j] = m[h][j];
+          static_cast<float*>(t.v)[i + j] = v[h][j];
+        }
+        if (t.copy) static_cast<uint16_t*>(t.copy)[i + j] = (uint16_t)f32_to_bf16_bits(p[h][j]);
+      }
+    }
+  }
+}
+
+hipError_t launch_adamw(const fp8q_adamw_tensor* tensors, int32_t count, const fp8q_adamw_args& h,
+                        int grad_bf16, int e4m3, hipStream_t stream) {
+  AdamwLaunch a;
+  a.lr = h.lr_dev;
+  a.step = h.step_dev;
+  a.grad_scale = h.grad_scale;
+  a.log_b1 = log(h.beta1);
+  a.log_b2 = log(h.beta2);
+  a.lr_host = h.lr;
+  a.decay = h.weight_decay;
+  a.b1 = (float)h.beta1;
+  a.one_b1 = (float)(1.0 - h.beta1);
+  a.b2 = (float)h.beta2;
+  a.one_b2 = (float)(1.0 - h.beta2);
+  a.eps = (float)h.eps;
+  a.keep = (float)(1.0 - h.lr * h.weight_decay);
+  // 1 - beta^t cancels for a beta near 1: from the logarithm, in 64 bits
+  const double c1 = -expm1((double)h.step * a.log_b1), c2 = -expm1((double)h.step * a.log_b2);
+  a.rate = (float)((h.lr_dev ? 1.0 : h.lr) / c1);
+  a.inv_root = (float)(1.0 / sqrt(c2));
+  a.dither = (uint32_t)h.step * kDitherStep;
+  auto kern = e4m3 ? (grad_bf16 ? adamw_kernel<true, true> : adamw_kernel<true, false>)
+                   : (grad_bf16 ? adamw_kernel<false, true> : adamw_kernel<false, false>);
+  int32_t i = 0;
+  while (i < count) {
+    int k = 0;
+    int64_t blocks = 0;
+    for (; i < count && k < kTensors; ++i) {
+      if (tensors[i].n == 0) continue;
+      const int64_t b = (tensors[i].n + kElems - 1) / kElems;
+      if (b > max_blocks(kThreads)) return hipErrorInvalidValue;
+      if (blocks + b > max_blocks(kThreads)) break;
+      a.t[k] = tensors[i];
+      a.first[k++] = (int32_t)blocks;
+      blocks += b;
+    }
+    if (k == 0) break;
+    for (int j = k; j < 64; ++j) a.first[j] = 0x7FFFFFFF;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp8q

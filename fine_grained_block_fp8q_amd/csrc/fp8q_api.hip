@@ -4,7 +4,9 @@
 // the header documents, so every error path can be exercised without a GPU.
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <atomic>
@@ -52,7 +54,32 @@ hipError_t launch_gemm_gated(const uint8_t* a_q, const float* a_s, int64_t M, co
 hipError_t launch_gated_backward(const void* dh, const void* gu, int64_t M, int64_t F, int act,
                                  int mode, uint8_t* q, float* s, uint8_t* qt, float* st,
                                  hipStream_t stream);
+hipError_t launch_layer_norm(const void* x, int x_bf16, const float* weight, const float* bias,
+                             int64_t M, int64_t N, float eps, void* y, int y_bf16, uint8_t* q,
+                             float* s, int mode, float* mean, float* rstd, hipStream_t stream);
+int64_t layer_norm_backward_workspace(int64_t M, int64_t N);
+hipError_t launch_layer_norm_backward(const void* dy, int dy_bf16, const void* x, int x_bf16,
+                                      const float* weight, const float* mean, const float* rstd,
+                                      int64_t M, int64_t N, void* dx, float* dweight, float* dbias,
+                                      float* workspace, hipStream_t stream);
+int64_t expert_columns(int64_t M, int64_t G);
+hipError_t launch_grouped_quantize_act_t(const void* x, int64_t M, int64_t K, const int32_t* off,
+                                         int G, uint8_t* qt, float* st, int mode,
+                                         hipStream_t stream);
+hipError_t launch_grouped_gated_backward(const void* dh, const void* gu, int64_t M,
+                                         const int32_t* off, int G, int64_t F, int act, int mode,
+                                         uint8_t* q, float* s, uint8_t* qt, float* st,
+                                         hipStream_t stream);
+hipError_t launch_grouped_gemm_rowscaled(const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                                         const float* b_s, int64_t T, const int32_t* off, int G,
+                                         int64_t N, int64_t K, void* c, int out_bf16, int precise,
+                                         hipStream_t stream);
+hipError_t launch_adamw(const fp8q_adamw_tensor* tensors, int32_t count, const fp8q_adamw_args& h,
+                        int grad_bf16, int e4m3, hipStream_t stream);
 #ifdef FP8Q_DEBUG_CHECKS
+hipError_t wgrad_offsets_error_take(hipStream_t stream, int* flag);
+hipError_t tokens_offsets_error_take(hipStream_t stream, int* flag);
+hipError_t backward_offsets_error_take(hipStream_t stream, int* flag);
 hipError_t offsets_error_take(hipStream_t stream, int* flag);
 hipError_t gated_offsets_error_take(hipStream_t stream, int* flag);
 #endif
@@ -95,19 +122,25 @@ fp8q_status launched(hipError_t e) {
 }
 
 // A grouped launch's status.  Debug builds (FP8Q_DEBUG_CHECKS) synchronize
-// the stream and report the kernel's verdict on the device offsets.
-fp8q_status grouped_launched(hipError_t e, hipStream_t stream, bool gated = false) {
+// the stream and report the verdict of kernel family `k` on the device offsets.
+enum Grouped { kGrouped, kGated, kWgrad, kTokens, kBackward };
+
+fp8q_status grouped_launched(hipError_t e, hipStream_t stream, Grouped k = kGrouped) {
   const fp8q_status st = launched(e);
 #ifdef FP8Q_DEBUG_CHECKS
   if (st == FP8Q_OK) {
     int flag = 0;
-    auto take = gated ? fp8q::gated_offsets_error_take : fp8q::offsets_error_take;
+    auto take = k == kGated      ? fp8q::gated_offsets_error_take
+                : k == kWgrad    ? fp8q::wgrad_offsets_error_take
+                : k == kTokens   ? fp8q::tokens_offsets_error_take
+                : k == kBackward ? fp8q::backward_offsets_error_take
+                                 : fp8q::offsets_error_take;
     if (take(stream, &flag) != hipSuccess) return launched(hipErrorUnknown);
     if (flag) return FP8Q_ERR_OFFSETS;
   }
 #else
   (void)stream;
-  (void)gated;
+  (void)k;
 #endif
   return st;
 }
@@ -470,7 +503,7 @@ static fp8q_status gated_call(const uint8_t* a_q, const float* a_s, int64_t M, b
   if (d != FP8Q_OK) return d;
   const hipError_t e = fp8q::launch_gemm_gated(a_q, a_s, M, off, G, w_q, w_s, F, K, act, h,
                                                out == FP8Q_OUT_BF16, gate_up, stream);
-  return grouped ? grouped_launched(e, stream, true) : launched(e);
+  return grouped ? grouped_launched(e, stream, kGated) : launched(e);
 }
 
 fp8q_status fp8q_gemm_gated(const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
@@ -503,6 +536,205 @@ fp8q_status fp8q_gated_backward(const void* dh, const void* gate_up, int64_t M, 
   const fp8q_status d = check_device();
   if (d != FP8Q_OK) return d;
   return launched(fp8q::launch_gated_backward(dh, gate_up, M, F, act, mode, q, s, qt, st, stream));
+}
+
+fp8q_status fp8q_layer_norm(const void* x, fp8q_out_dtype x_type, const float* weight,
+                            const float* bias, int64_t M, int64_t N, float eps, void* y,
+                            fp8q_out_dtype y_type, uint8_t* q, float* s, fp8q_scale_mode mode,
+                            float* mean, float* rstd, hipStream_t stream) {
+  const bool empty = M == 0;
+  if (!empty && (!x || !weight || !mean || !rstd || !q != !s || (!y && !q))) return FP8Q_ERR_NULL;
+  if (M < 0 || N < 1 || (q && N % 128 != 0)) return FP8Q_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(q, 16) || !aligned(weight, 4) ||
+      !aligned(bias, 4) || !aligned(s, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_out(x_type) || !valid_out(y_type) || !valid_mode(mode)) return FP8Q_ERR_ENUM;
+  if (N > 16384 || !(eps >= 0.f) || !isfinite(eps)) return FP8Q_ERR_UNSUPPORTED;
+  if (empty) return FP8Q_OK;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return launched(fp8q::launch_layer_norm(x, x_type == FP8Q_OUT_BF16, weight, bias, M, N, eps, y,
+                                          y_type == FP8Q_OUT_BF16, q, s, mode, mean, rstd,
+                                          stream));
+}
+
+int64_t fp8q_layer_norm_backward_workspace(int64_t M, int64_t N) {
+  return M > 0 && N > 0 && N <= 16384 ? fp8q::layer_norm_backward_workspace(M, N) : 0;
+}
+
+fp8q_status fp8q_layer_norm_backward(const void* dy, fp8q_out_dtype dy_type, const void* x,
+                                     fp8q_out_dtype x_type, const float* weight,
+                                     const float* mean, const float* rstd, int64_t M, int64_t N,
+                                     void* dx, float* dweight, float* dbias, void* workspace,
+                                     hipStream_t stream) {
+  if (!dweight) return FP8Q_ERR_NULL;
+  if (M != 0 && (!dy || !x || !weight || !mean || !rstd || !dx || !workspace))
+    return FP8Q_ERR_NULL;
+  if (M < 0 || N < 1) return FP8Q_ERR_SHAPE;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(workspace, 16) ||
+      !aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) ||
+      !aligned(dbias, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_out(dy_type) || !valid_out(x_type)) return FP8Q_ERR_ENUM;
+  if (N > 16384) return FP8Q_ERR_UNSUPPORTED;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return launched(fp8q::launch_layer_norm_backward(
+      dy, dy_type == FP8Q_OUT_BF16, x, x_type == FP8Q_OUT_BF16, weight, mean, rstd, M, N, dx,
+      dweight, dbias, static_cast<float*>(workspace), stream));
+}
+
+int64_t fp8q_expert_columns(int64_t M_total, int32_t G) {
+  return M_total > 0 && G > 0 ? fp8q::expert_columns(M_total, G) : 0;
+}
+
+fp8q_status fp8q_grouped_quantize_act_t(const void* x_bf16, int64_t M_total, const int32_t* off,
+                                        int32_t G, int64_t K, uint8_t* q_t, float* s_t,
+                                        fp8q_scale_mode mode, hipStream_t stream) {
+  const bool empty = (M_total == 0 || K == 0);
+  if (!off || (!empty && (!x_bf16 || !q_t || !s_t))) return FP8Q_ERR_NULL;
+  if (M_total < 0 || M_total > 0x7FFFFFFF || K < 0 || K % 128 != 0 || G < 1) return FP8Q_ERR_SHAPE;
+  if (!aligned(x_bf16, 16) || !aligned(q_t, 16) || !aligned(s_t, 4) || !aligned(off, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_mode(mode)) return FP8Q_ERR_ENUM;
+  if (G > 1024 || K > (int64_t(1) << 22)) return FP8Q_ERR_UNSUPPORTED;  // 32-bit offsets
+  if (empty) return FP8Q_OK;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return grouped_launched(
+      fp8q::launch_grouped_quantize_act_t(x_bf16, M_total, K, off, G, q_t, s_t, mode, stream),
+      stream, kTokens);
+}
+
+fp8q_status fp8q_grouped_gated_backward(const void* dh, const void* gate_up, int64_t M_total,
+                                        const int32_t* off, int32_t G, int64_t F,
+                                        fp8q_activation act, fp8q_scale_mode mode, uint8_t* q,
+                                        float* s, uint8_t* qt, float* st, hipStream_t stream) {
+  const bool empty = (M_total == 0 || F == 0);
+  if (!off || (!empty && (!dh || !gate_up || !q != !s || !qt != !st || (!q && !qt))))
+    return FP8Q_ERR_NULL;
+  if (M_total < 0 || M_total > 0x7FFFFFFF || F < 0 || F % 128 != 0 || G < 1) return FP8Q_ERR_SHAPE;
+  if (!aligned(dh, 16) || !aligned(gate_up, 16) || !aligned(q, 16) || !aligned(qt, 16) ||
+      !aligned(s, 4) || !aligned(st, 4) || !aligned(off, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_act(act) || !valid_mode(mode)) return FP8Q_ERR_ENUM;
+  if (G > 1024 || F > (int64_t(1) << 22)) return FP8Q_ERR_UNSUPPORTED;  // 32-bit offsets
+  if (empty) return FP8Q_OK;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return grouped_launched(fp8q::launch_grouped_gated_backward(dh, gate_up, M_total, off, G, F, act,
+                                                              mode, q, s, qt, st, stream),
+                          stream, kBackward);
+}
+
+static fp8q_status grouped_rowscaled_call(const uint8_t* a_q, const float* a_s,
+                                          const uint8_t* b_q, const float* b_s, int64_t T,
+                                          const int32_t* off, int32_t G, int64_t N, int64_t K,
+                                          void* c, int out, int precise, hipStream_t stream) {
+  const bool empty_out = (N == 0 || K == 0);
+  if (!off || (!empty_out && !c)) return FP8Q_ERR_NULL;
+  if (!empty_out && T != 0 && (!a_q || !a_s || !b_q || !b_s)) return FP8Q_ERR_NULL;
+  if (T < 0 || N < 0 || K < 0 || T % 128 != 0 || N % 128 != 0 || K % 128 != 0 || G < 1)
+    return FP8Q_ERR_SHAPE;
+  if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(c, 16) || !aligned(a_s, 4) ||
+      !aligned(b_s, 4) || !aligned(off, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_out(out)) return FP8Q_ERR_ENUM;
+  // 32-bit offsets within a tile's rows of T bytes
+  if (G > 1024 || T > (int64_t(1) << 24)) return FP8Q_ERR_UNSUPPORTED;
+  if (empty_out) return FP8Q_OK;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return grouped_launched(
+      fp8q::launch_grouped_gemm_rowscaled(a_q, a_s, b_q, b_s, T, off, G, N, K, c,
+                                          out == FP8Q_OUT_BF16, precise, stream),
+      stream, kWgrad);
+}
+
+fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                                        const float* b_s, int64_t T, const int32_t* off,
+                                        int32_t G, int64_t N, int64_t K, void* c,
+                                        fp8q_out_dtype out, hipStream_t stream) {
+  return grouped_rowscaled_call(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out, 0, stream);
+}
+
+fp8q_status fp8q_grouped_gemm_rowscaled_precise(const uint8_t* a_q, const float* a_s,
+                                                const uint8_t* b_q, const float* b_s, int64_t T,
+                                                const int32_t* off, int32_t G, int64_t N,
+                                                int64_t K, void* c, fp8q_out_dtype out,
+                                                hipStream_t stream) {
+  return grouped_rowscaled_call(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out, 1, stream);
+}
+
+// Whether two tensors' p overlap.  A short list is compared pair by pair, a long
+// one in the order of its addresses.
+static bool p_before(const fp8q_adamw_tensor* a, const fp8q_adamw_tensor* b) {
+  return a->n == 0 || b->n == 0 || reinterpret_cast<uintptr_t>(a->p + a->n) <=
+                                       reinterpret_cast<uintptr_t>(b->p);
+}
+
+static int by_p(const void* x, const void* y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>((*static_cast<const fp8q_adamw_tensor* const*>(x))->p);
+  const uintptr_t b = reinterpret_cast<uintptr_t>((*static_cast<const fp8q_adamw_tensor* const*>(y))->p);
+  return a < b ? -1 : a > b;
+}
+
+static fp8q_status check_overlap(const fp8q_adamw_tensor* t, int32_t count) {
+  if (count <= 64) {
+    for (int32_t i = 1; i < count; ++i)
+      for (int32_t j = 0; j < i; ++j)
+        if (!p_before(t + i, t + j) && !p_before(t + j, t + i)) return FP8Q_ERR_UNSUPPORTED;
+    return FP8Q_OK;
+  }
+  auto** order = static_cast<const fp8q_adamw_tensor**>(malloc(sizeof(void*) * (size_t)count));
+  if (!order) return FP8Q_ERR_LAUNCH;
+  int32_t n = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (t[i].n > 0) order[n++] = t + i;
+  qsort(order, (size_t)n, sizeof *order, by_p);
+  bool apart = true;
+  for (int32_t i = 1; i < n; ++i) apart = apart && p_before(order[i - 1], order[i]);
+  free(order);
+  return apart ? FP8Q_OK : FP8Q_ERR_UNSUPPORTED;
+}
+
+static bool not_negative(double v) { return v >= 0.0 && isfinite(v); }
+
+fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int32_t count,
+                       const fp8q_adamw_args* args, fp8q_out_dtype grad_type,
+                       fp8q_moments moments, hipStream_t stream) {
+  const bool e4m3 = moments == FP8Q_MOMENTS_E4M3;
+  if (!args || (count > 0 && !tensors)) return FP8Q_ERR_NULL;
+  int64_t work = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const fp8q_adamw_tensor& t = tensors[i];
+    if (t.n > 0 && (!t.p || !t.g || !t.m || !t.v || (e4m3 && (!t.m_s || !t.v_s))))
+      return FP8Q_ERR_NULL;
+  }
+  if (count < 0) return FP8Q_ERR_SHAPE;
+  for (int32_t i = 0; i < count; ++i)
+    if (tensors[i].n < 0) return FP8Q_ERR_SHAPE;
+  for (int32_t i = 0; i < count; ++i) {
+    const fp8q_adamw_tensor& t = tensors[i];
+    if (!aligned(t.p, 16) || !aligned(t.g, 16) || !aligned(t.m, 16) || !aligned(t.v, 16) ||
+        !aligned(t.copy, 16) || !aligned(t.m_s, 4) || !aligned(t.v_s, 4))
+      return FP8Q_ERR_ALIGN;
+    work |= t.n;
+  }
+  if (!aligned(args->lr_dev, 4) || !aligned(args->step_dev, 4) || !aligned(args->grad_scale, 4))
+    return FP8Q_ERR_ALIGN;
+  if (!valid_out(grad_type) || (moments != FP8Q_MOMENTS_F32 && !e4m3)) return FP8Q_ERR_ENUM;
+  if ((!args->lr_dev && !not_negative(args->lr)) || !not_negative(args->eps) ||
+      !not_negative(args->weight_decay) || !(args->beta1 >= 0.0 && args->beta1 < 1.0) ||
+      !(args->beta2 >= 0.0 && args->beta2 < 1.0) || (!args->step_dev && args->step < 1))
+    return FP8Q_ERR_UNSUPPORTED;
+  if (work == 0) return FP8Q_OK;
+  const fp8q_status o = check_overlap(tensors, count);
+  if (o != FP8Q_OK) return o;
+  const fp8q_status d = check_device();
+  if (d != FP8Q_OK) return d;
+  return launched(fp8q::launch_adamw(tensors, count, *args, grad_type == FP8Q_OUT_BF16, e4m3,
+                                     stream));
 }
 
 }  // extern "C"

@@ -34,10 +34,15 @@
 //
 // Tokens past M count as zeros: the last group of tokens is a full one, and its
 // codes past M are zero.
+//
+// By expert (EXPERTS): the groups of tokens are those of experts.hpp, of which each
+// expert's last one may end early; everything else is the same.  Rows past the
+// last expert are in no group, and their codes along the features not written.
 
 #include <type_traits>
 
 #include "activation.hpp"
+#include "experts.hpp"
 #include "gemm_common.hpp"
 #include "launch.hpp"
 #include "quant_rules.hpp"
@@ -125,20 +130,16 @@ struct BwShared {
   uint8_t tile[2][128 * 128];
 };
 
+// Group of tokens tb: its first row mb and its number of rows `live`.
 template <int MODE, int ACT>
 __device__ __forceinline__ void gated_backward(
     const uint16_t* dh, const uint16_t* gu, int64_t M, int64_t F, uint8_t* q, float* s, uint8_t* qt,
-    float* st, int64_t Mp, int n_fblk, BwShared& sh) {
-  const int fb = blockIdx.x % n_fblk;
-  const int64_t tb = blockIdx.x / n_fblk;
+    float* st, int64_t Mp, int fb, int64_t tb, int64_t mb, int live, BwShared& sh) {
   const int t = threadIdx.x, l16 = t & 15, rq = t >> 4, wave = t >> 6;
-  const int64_t m0 = tb * kGroup + 4 * rq;
   const int64_t f0 = (int64_t)fb * kGroup + 8 * l16;
 
-  // Byte offsets within the block's 128 tokens; of tokens past M loads deliver
+  // Byte offsets within the block's 128 tokens; of tokens past `live` loads deliver
   // zeros and stores are dropped (they are out of the resources' range).
-  const int64_t mb = tb * kGroup;
-  const int live = __builtin_amdgcn_readfirstlane(M - mb < kGroup ? (int)(M - mb) : kGroup);
   const __amdgpu_buffer_rsrc_t rd = make_rsrc(dh + mb * F, live * F * 2);
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(gu + mb * 2 * F, live * F * 4);
   const int fs = (int)F;
@@ -172,8 +173,8 @@ __device__ __forceinline__ void gated_backward(
       }
     const GroupRule mine = group_rule<MODE>(amax);
     const __amdgpu_buffer_rsrc_t rq_ = make_rsrc(q + mb * 2 * F, live * F * 2);
-    if (l16 < 8 && m0 + (l16 & 3) < M)
-      s[((l16 >> 2) * (F / kGroup) + fb) * M + m0 + (l16 & 3)] = mine.s;
+    const int r = 4 * rq + (l16 & 3);
+    if (l16 < 8 && r < live) s[((l16 >> 2) * (F / kGroup) + fb) * M + mb + r] = mine.s;
     auto each = [&](auto hi) {  // (the lane to broadcast from is an immediate)
       constexpr int h = decltype(hi)::value / 4, i = decltype(hi)::value % 4;
       const GroupRule r = rule_of_lane<MODE, decltype(hi)::value>(mine);
@@ -241,25 +242,38 @@ __device__ __forceinline__ void gated_backward(
   }
 }
 
-template <int MODE, int ACT>
+template <int MODE, int ACT, bool EXPERTS>
 __global__ __launch_bounds__(kBwThreads) void gated_backward_kernel(
     const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu, int64_t M, int64_t F,
-    uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
-    float* __restrict__ st, int64_t Mp, int n_fblk) {
+    const int32_t* __restrict__ off, int G, uint8_t* __restrict__ q, float* __restrict__ s,
+    uint8_t* __restrict__ qt, float* __restrict__ st, int64_t Mp, int n_fblk) {
   __shared__ __attribute__((aligned(16))) BwShared sh;
-  gated_backward<MODE, ACT>(dh, gu, M, F, q, s, qt, st, Mp, n_fblk, sh);
+  const int fb = blockIdx.x % n_fblk;
+  const int64_t tb = blockIdx.x / n_fblk;
+  int64_t mb = tb * kGroup;
+  int live = __builtin_amdgcn_readfirstlane(M - mb < kGroup ? (int)(M - mb) : kGroup);
+  if constexpr (EXPERTS) {
+    const ExpertSpan span = expert_span<true>(off, G, M, Mp / kGroup, (int)tb);
+    if (invalid(span)) return;
+    mb = span.first;
+    live = span.rows;
+  }
+  gated_backward<MODE, ACT>(dh, gu, M, F, q, s, qt, st, Mp, fb, tb, mb, live, sh);
 }
 
 // ---- few groups: each form by workgroups of its own, in small pieces
 
 // Rows' form of 16 tokens x 128 features: lane (t/16, t%16) owns token t/16 at
-// features 8 (t%16) .. +7.
+// features 8 (t%16) .. +7.  Rows past `end` are left out.
 template <int MODE, int ACT>
 __device__ __forceinline__ void backward_rows(const uint16_t* dh, const uint16_t* gu, int64_t M,
-                                              int64_t F, uint8_t* q, float* s, int64_t tb, int fb) {
+                                              int64_t end, int64_t F, uint8_t* q, float* s,
+                                              int64_t tb, int fb) {
   const int t = threadIdx.x, l16 = t & 15, row = t >> 4;
   const int64_t mb = tb * kRowsTokens;
-  const int live = __builtin_amdgcn_readfirstlane(M - mb < kRowsTokens ? (int)(M - mb) : kRowsTokens);
+  if (mb >= end) return;
+  const int live =
+      __builtin_amdgcn_readfirstlane(end - mb < kRowsTokens ? (int)(end - mb) : kRowsTokens);
   const int fs = (int)F, f0 = fb * kGroup + 8 * l16;
   const __amdgpu_buffer_rsrc_t rd = make_rsrc(dh + mb * F, live * F * 2);
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(gu + mb * 2 * F, live * F * 4);
@@ -298,12 +312,10 @@ struct TokensShared {
 // Tokens' form of 128 tokens x 32 features: lane (t/8, t%8) owns tokens
 // 4 (t/8) .. +3 at features 4 (t%8) .. +3.
 template <int MODE, int ACT>
-__device__ __forceinline__ void backward_tokens(const uint16_t* dh, const uint16_t* gu, int64_t M,
-                                                int64_t F, uint8_t* qt, float* st, int64_t Mp,
-                                                int64_t tb, int fb, TokensShared& sh) {
+__device__ __forceinline__ void backward_tokens(const uint16_t* dh, const uint16_t* gu, int64_t mb,
+                                                int live, int64_t F, uint8_t* qt, float* st,
+                                                int64_t Mp, int64_t tb, int fb, TokensShared& sh) {
   const int t = threadIdx.x, l8 = t & 7, rq = t >> 3, wave = t >> 6;
-  const int64_t mb = tb * kGroup;
-  const int live = __builtin_amdgcn_readfirstlane(M - mb < kGroup ? (int)(M - mb) : kGroup);
   const int fs = (int)F, f0 = fb * kTokensFeatures;
   const __amdgpu_buffer_rsrc_t rd = make_rsrc(dh + mb * F, live * F * 2);
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(gu + mb * 2 * F, live * F * 4);
@@ -355,52 +367,83 @@ __device__ __forceinline__ void backward_tokens(const uint16_t* dh, const uint16
   const int c = t >> 3, piece = t & 7;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    *reinterpret_cast<v4u*>(qt + (h * F + f0 + c) * Mp + mb + 16 * piece) =
+    *reinterpret_cast<v4u*>(qt + (h * F + f0 + c) * Mp + tb * kGroup + 16 * piece) =
         *reinterpret_cast<const v4u*>(sh.tile[h] + at(c, 4 * piece));
 }
 
 // The first n_rows workgroups take the rows' form, the others the tokens'.
-template <int MODE, int ACT>
+template <int MODE, int ACT, bool EXPERTS>
 __global__ __launch_bounds__(kSmallThreads) void gated_backward_small_kernel(
     const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu, int64_t M, int64_t F,
-    uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
-    float* __restrict__ st, int64_t Mp, int n_fblk, int n_rows) {
+    const int32_t* __restrict__ off, int G, uint8_t* __restrict__ q, float* __restrict__ s,
+    uint8_t* __restrict__ qt, float* __restrict__ st, int64_t Mp, int n_fblk, int n_rows) {
   __shared__ __attribute__((aligned(16))) TokensShared sh;
   const int b = blockIdx.x;
-  if (b < n_rows) {
-    backward_rows<MODE, ACT>(dh, gu, M, F, q, s, b / n_fblk, b % n_fblk);
-  } else {
-    const int n = n_fblk * (kGroup / kTokensFeatures), c = b - n_rows;
-    backward_tokens<MODE, ACT>(dh, gu, M, F, qt, st, Mp, c / n, c % n, sh);
+  const int n = n_fblk * (kGroup / kTokensFeatures), c = b - n_rows;
+  const int64_t tb = b < n_rows ? b / n_fblk : c / n;
+  int64_t mb = tb * kGroup, end = M;
+  int live = __builtin_amdgcn_readfirstlane(M - mb < kGroup ? (int)(M - mb) : kGroup);
+  if constexpr (EXPERTS) {
+    const ExpertSpan span = expert_span<true>(off, G, M, Mp / kGroup, (int)tb);
+    if (invalid(span)) return;
+    mb = span.first;
+    live = span.rows;
+    end = off[G];
   }
+  if (b < n_rows)
+    backward_rows<MODE, ACT>(dh, gu, M, end, F, q, s, tb, b % n_fblk);
+  else
+    backward_tokens<MODE, ACT>(dh, gu, mb, live, F, qt, st, Mp, tb, c % n, sh);
 }
 
-hipError_t launch_gated_backward(const void* dh, const void* gu, int64_t M, int64_t F, int act,
-                                 int mode, uint8_t* q, float* s, uint8_t* qt, float* st,
-                                 hipStream_t stream) {
-  const int64_t n_fblk = F / kGroup, tb = (M + kGroup - 1) / kGroup;
+// off NULL: the dense call.
+template <bool EXPERTS>
+static hipError_t launch(const void* dh, const void* gu, int64_t M, const int32_t* off, int G,
+                         int64_t F, int act, int mode, uint8_t* q, float* s, uint8_t* qt,
+                         float* st, hipStream_t stream) {
+  const int64_t n_fblk = F / kGroup;
+  const int64_t tb = EXPERTS ? expert_groups_most(M, G) : (M + kGroup - 1) / kGroup;
   if (n_fblk * tb > max_blocks(kBwThreads)) return hipErrorInvalidValue;
   if (n_fblk * tb <= kSmallBlocks) {
     const int64_t n_rows = q ? (M + kRowsTokens - 1) / kRowsTokens * n_fblk : 0;
     const int64_t n = n_rows + (qt ? tb * n_fblk * (kGroup / kTokensFeatures) : 0);
     auto kern = act == kActSilu
-                    ? (mode == 0 ? gated_backward_small_kernel<0, kActSilu>
-                                 : gated_backward_small_kernel<1, kActSilu>)
-                    : (mode == 0 ? gated_backward_small_kernel<0, kActGeluTanh>
-                                 : gated_backward_small_kernel<1, kActGeluTanh>);
+                    ? (mode == 0 ? gated_backward_small_kernel<0, kActSilu, EXPERTS>
+                                 : gated_backward_small_kernel<1, kActSilu, EXPERTS>)
+                    : (mode == 0 ? gated_backward_small_kernel<0, kActGeluTanh, EXPERTS>
+                                 : gated_backward_small_kernel<1, kActGeluTanh, EXPERTS>);
     hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(kSmallThreads), 0, stream,
-                       static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gu), M, F, q,
-                       s, qt, st, tb * kGroup, (int)n_fblk, (int)n_rows);
+                       static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gu), M, F,
+                       off, G, q, s, qt, st, tb * kGroup, (int)n_fblk, (int)n_rows);
     return hipGetLastError();
   }
-  auto kern = act == kActSilu
-                  ? (mode == 0 ? gated_backward_kernel<0, kActSilu> : gated_backward_kernel<1, kActSilu>)
-                  : (mode == 0 ? gated_backward_kernel<0, kActGeluTanh>
-                               : gated_backward_kernel<1, kActGeluTanh>);
+  auto kern = act == kActSilu ? (mode == 0 ? gated_backward_kernel<0, kActSilu, EXPERTS>
+                                           : gated_backward_kernel<1, kActSilu, EXPERTS>)
+                              : (mode == 0 ? gated_backward_kernel<0, kActGeluTanh, EXPERTS>
+                                           : gated_backward_kernel<1, kActGeluTanh, EXPERTS>);
   hipLaunchKernelGGL(kern, dim3((unsigned)(n_fblk * tb)), dim3(kBwThreads), 0, stream,
-                     static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gu), M, F, q,
-                     s, qt, st, tb * kGroup, (int)n_fblk);
+                     static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gu), M, F, off,
+                     G, q, s, qt, st, tb * kGroup, (int)n_fblk);
   return hipGetLastError();
 }
+
+hipError_t launch_gated_backward(const void* dh, const void* gu, int64_t M, int64_t F, int act,
+                                 int mode, uint8_t* q, float* s, uint8_t* qt, float* st,
+                                 hipStream_t stream) {
+  return launch<false>(dh, gu, M, nullptr, 0, F, act, mode, q, s, qt, st, stream);
+}
+
+hipError_t launch_grouped_gated_backward(const void* dh, const void* gu, int64_t M,
+                                         const int32_t* off, int G, int64_t F, int act, int mode,
+                                         uint8_t* q, float* s, uint8_t* qt, float* st,
+                                         hipStream_t stream) {
+  return launch<true>(dh, gu, M, off, G, F, act, mode, q, s, qt, st, stream);
+}
+
+#ifdef FP8Q_DEBUG_CHECKS
+hipError_t backward_offsets_error_take(hipStream_t stream, int* flag) {
+  return take_experts_error(stream, flag);
+}
+#endif
 
 }  // namespace fp8q

@@ -473,6 +473,168 @@ fp8q_status fp8q_gated_backward(const void* dh, const void* gate_up, int64_t M, 
                                 fp8q_activation act, fp8q_scale_mode mode, uint8_t* q, float* s,
                                 uint8_t* qt, float* st, hipStream_t stream);
 
+/*
+ * The rest of a training step around the FP8 products (the calls below): layer
+ * norm and its backward pass, the gradients of experts' weights, and AdamW.
+ */
+
+/*
+ * Layer norm of rows: z = (x - mean) * rstd, rstd = 1 / sqrt(var + eps), var the
+ * mean square of x - mean; y = z * weight + bias, in FP32 and rounded once.
+ *   x      : [M][N] float32 or bfloat16 (per `x_type`), row-major; 16-byte aligned.
+ *   weight : [N] float32; bias: [N] float32, or NULL for none.
+ *   y      : [M][N] float32 or bfloat16 (per `y_type`) (output), or NULL.
+ *   q, s   : y in 1x128 groups by the rule of fp8q_quantize_act (from y in FP32,
+ *            not from its BF16 rounding): [M][N] codes, 16-byte aligned, and
+ *            [N/128][M] scales (output); or both NULL.  One of y and q is wanted.
+ *   mean, rstd : [M] float32 (output).
+ *   M >= 0, 1 <= N <= 16384 (more: FP8Q_ERR_UNSUPPORTED); with q, N % 128 == 0.
+ *   eps >= 0, finite (else FP8Q_ERR_UNSUPPORTED).
+ * ACCURACY.  mean and var are FP32 sums over the row, var about the mean.  With u =
+ * 2^-24 and D = 40 u mean|x|:
+ *   |mean - mean_exact| <= D,  rstd within 23 u + (D rstd)^2 / 2 relative,
+ *   |z - z_exact| <= rstd D + (25 u + (D rstd)^2 / 2) |z|,  and y within
+ *   |weight| times that + 2 u |z weight| + u |y| (and half a BF16 ulp).
+ */
+fp8q_status fp8q_layer_norm(const void* x, fp8q_out_dtype x_type, const float* weight,
+                            const float* bias, int64_t M, int64_t N, float eps, void* y,
+                            fp8q_out_dtype y_type, uint8_t* q, float* s, fp8q_scale_mode mode,
+                            float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * Backward pass of layer norm.  With z as above and gz = dy * weight:
+ *   dx = rstd * (gz - mean(gz) - z * mean(gz * z))     (means over the row),
+ *   dweight[n] = sum over rows of dy * z,  dbias[n] = sum over rows of dy.
+ *   dy     : [M][N] float32 or bfloat16 (per `dy_type`); x as above, mean and rstd
+ *            as fp8q_layer_norm wrote them.
+ *   dx     : [M][N] of x's type (output); dweight: [N] float32 (output); dbias:
+ *            [N] float32 (output), or NULL.
+ *   workspace : fp8q_layer_norm_backward_workspace(M, N) bytes, 16-byte aligned,
+ *            whose contents do not matter before or after the call; calls that can
+ *            run at the same time need one each.  NULL where that is 0.
+ *   M >= 0 (with M == 0 dweight and dbias are zeros), N and x as above.
+ * The sums over rows are FP32 in a fixed order: the same bits every time.
+ */
+int64_t fp8q_layer_norm_backward_workspace(int64_t M, int64_t N);
+fp8q_status fp8q_layer_norm_backward(const void* dy, fp8q_out_dtype dy_type, const void* x,
+                                     fp8q_out_dtype x_type, const float* weight,
+                                     const float* mean, const float* rstd, int64_t M, int64_t N,
+                                     void* dx, float* dweight, float* dbias, void* workspace,
+                                     hipStream_t stream);
+
+/*
+ * Tokens by expert, transposed.  The weight gradient of expert e sums over its
+ * tokens, rows [off[e], off[e+1]), so its operands carry scales in groups of 128
+ * of them.  Expert e's n_e rows take ceil(n_e/128) groups, which follow those of
+ * expert e-1: no group holds two experts' tokens.  An operand has
+ *   T = fp8q_expert_columns(M_total, G) columns, 128 times the most groups that
+ * M_total rows in G experts can take; those past an expert's last row, and past the
+ * last expert, hold zero codes (groups past the last expert zero scales).
+ * off is a DEVICE int32[G+1], 0 = off[0] <= ... <= off[G] <= M_total, checked on the
+ * device: with invalid offsets these calls write nothing and return FP8Q_OK (debug
+ * builds: FP8Q_ERR_OFFSETS), as fp8q_grouped_gemm does.  G <= 1024 (more:
+ * FP8Q_ERR_UNSUPPORTED).
+ */
+int64_t fp8q_expert_columns(int64_t M_total, int32_t G);
+
+/* fp8q_quantize_act_t by expert.
+ *   x_bf16 : [M_total][K] bfloat16; 16-byte aligned.
+ *   q_t    : [K][T] codes (output); s_t : [T/128][K] float32 (output).
+ *   K % 128 == 0, K <= 2^22 (more: FP8Q_ERR_UNSUPPORTED). */
+fp8q_status fp8q_grouped_quantize_act_t(const void* x_bf16, int64_t M_total, const int32_t* off,
+                                        int32_t G, int64_t K, uint8_t* q_t, float* s_t,
+                                        fp8q_scale_mode mode, hipStream_t stream);
+
+/* fp8q_gated_backward by expert: qt [2F][T] and st [T/128][2F] have the groups of
+ * tokens above, q and s are as there (rows past off[G] are left untouched). */
+fp8q_status fp8q_grouped_gated_backward(const void* dh, const void* gate_up, int64_t M_total,
+                                        const int32_t* off, int32_t G, int64_t F,
+                                        fp8q_activation act, fp8q_scale_mode mode, uint8_t* q,
+                                        float* s, uint8_t* qt, float* st, hipStream_t stream);
+
+/*
+ * Weight gradients of all experts: fp8q_gemm_rowscaled over each expert's groups,
+ *   C[e][n][k] = sum over expert e's groups g of (a_s[g][n] * b_s[g][k]) * P_g[n][k].
+ *   a_q : [N][T] uint8, a_s : [T/128][N] float32; b_q : [K][T] uint8, b_s : [T/128][K]
+ *         float32 (both as from the calls above, with the same off)
+ *   T   : the operands' columns, a multiple of 128, at least the groups that off
+ *         asks for (fewer: invalid offsets).
+ *   c   : [G][N][K] float32 or bfloat16 (per `out`) (output); zeros for an expert
+ *         without rows.
+ *   N % 128 == 0, K % 128 == 0.  FP8Q_ERR_UNSUPPORTED: G > 1024, T > 2^24 (32-bit
+ *   load offsets).
+ * Accuracy: the ACCURACY clause of fp8q_gemm over each expert's groups, and for the
+ * precise call that of fp8q_gemm_precise.
+ */
+fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
+                                        const float* b_s, int64_t T, const int32_t* off,
+                                        int32_t G, int64_t N, int64_t K, void* c,
+                                        fp8q_out_dtype out, hipStream_t stream);
+fp8q_status fp8q_grouped_gemm_rowscaled_precise(const uint8_t* a_q, const float* a_s,
+                                                const uint8_t* b_q, const float* b_s, int64_t T,
+                                                const int32_t* off, int32_t G, int64_t N,
+                                                int64_t K, void* c, fp8q_out_dtype out,
+                                                hipStream_t stream);
+
+/*
+ * One AdamW step over many tensors, in place.  With g the gradient times
+ * *grad_scale (1 where that is NULL) and t the step's number, in FP32:
+ *   m = fl(fl(beta1 m) + fl((1 - beta1) g)),
+ *   v = fl(fl(beta2 v) + fl((1 - beta2) fl(g g))),
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps);
+ * the factors of lr, weight_decay and t are formed in 64 bits and rounded once.
+ *
+ * Moments in E4M3 (FP8Q_MOMENTS_E4M3): m holds codes of m and v codes of r = sqrt(v),
+ * each 128 consecutive elements of a tensor (the last ones fewer) with one scale,
+ * m_s and v_s: fl(amax * fl(1/448)) of their largest magnitude amax, multiplier
+ * fl(448 * fl(1/amax)) (not finite: scale and codes are 0).  m = code * scale, v =
+ * fl(r r), r = code * scale go into the formulas above; then x = fl(m * multiplier)
+ * and the same of r are rounded with a dither instead of to the nearest, so that a
+ * moment that moves by less than a code's step each time does not stay where it is.
+ * |x| becomes the E4M3 value at or below it, or the next one where |x|'s fraction of
+ * that step, in units of 2^-20, and u reach 2^20, with
+ *   u = (i * 0x85EBCA6B + t * 0x9E3779B1 mod 2^32) >> 12
+ * of the element's place i in its tensor and the step's number for m, 2^20 - 1 - u
+ * for r; a r that is not zero becomes 2^-9 at least.  (The fraction is of FP32's bits:
+ * below 2^-6, of |x| + 2^-6 rounded to FP32.)
+ */
+typedef enum {
+  FP8Q_MOMENTS_F32 = 0,  /* m, v: float32 [n]                                       */
+  FP8Q_MOMENTS_E4M3 = 1  /* m, v: uint8 codes [n]; m_s, v_s: float32 [ceil(n/128)]   */
+} fp8q_moments;
+
+typedef struct {
+  float* p;       /* master weights [n] (in and out)                                */
+  const void* g;  /* gradient [n], float32 or bfloat16                              */
+  void* m;        /* first moment (in and out)                                      */
+  void* v;        /* second moment, or the codes of its root (in and out)           */
+  float* m_s;     /* scales of m and v: E4M3 moments only                           */
+  float* v_s;
+  void* copy;     /* p as bfloat16 [n] (output), or NULL                            */
+  int64_t n;      /* elements; 0: nothing to do                                     */
+} fp8q_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;             /* t, 1 for the first step                                */
+  const float* lr_dev;      /* DEVICE float32[1] in lr's place, or NULL               */
+  const int32_t* step_dev;  /* DEVICE int32[1] (>= 1) in step's place, or NULL        */
+  const float* grad_scale;  /* DEVICE float32[1], or NULL                             */
+} fp8q_adamw_args;
+
+/*
+ *   tensors : HOST array of `count` descriptions, read during the call.
+ *   All data pointers 16-byte aligned, scales and the device scalars 4-byte.
+ * A captured call keeps host values: a graph that is replayed step after step takes
+ * its step's number (and a changing lr) from the device.
+ * FP8Q_ERR_UNSUPPORTED: two tensors' p overlap, a beta outside [0, 1), lr, eps or
+ * weight_decay negative or not finite, or step < 1 (without step_dev).
+ * No other memory of one call may overlap.
+ */
+fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int32_t count,
+                       const fp8q_adamw_args* args, fp8q_out_dtype grad_type,
+                       fp8q_moments moments, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* fp8q_status_string(fp8q_status status);
 

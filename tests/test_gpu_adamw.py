@@ -1,0 +1,296 @@
+"""AdamW on the GPU.  Moments and their codes and scales are held bit for bit to the
+call's FP32 operations (oracle.training_step).  The new parameter is held to
+float64 from those moments: p (1 - lr wd) with a rounded factor, product and
+difference 3 u |p|; the update is three rounded factors, a product, a quotient and
+a root's product and sum, each within u (the root itself half a unit), and one
+more for the difference: 8 u of it; half an ulp of BF16 (2^-8) for the copy."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV, fq, host
+from oracle import training_step as ots
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HYPER = dict(lr=3e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1)
+
+
+def _f32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(DEV)
+
+
+class Tensors:
+    """Tensors of the given sizes: host copies, and the device's."""
+
+    def __init__(self, sizes, eight, grad, seed=0, zero=False, step=1):
+        rng = np.random.default_rng([seed, len(sizes), eight])
+        self.eight, self.sizes = eight, sizes
+        spread = lambda n: np.exp(rng.uniform(-6, 0, n))   # noqa: E731
+        self.p = [rng.standard_normal(n).astype(np.float32) for n in sizes]
+        self.g = [(1e-3 * rng.standard_normal(n) * spread(n)).astype(np.float32) for n in sizes]
+        root = [np.abs(1e-3 * spread(n)).astype(np.float32) * (not zero) for n in sizes]
+        m = [(0.3 * r * rng.standard_normal(r.size)).astype(np.float32) for r in root]
+        self.gd = [_f32(g).to(torch.bfloat16 if grad == "bf16" else torch.float32) for g in self.g]
+        self.g = [host(g.float()) for g in self.gd]
+        self.pd = [_f32(p) for p in self.p]
+        if eight:
+            self.mq, self.ms = zip(*[ots.encode_moments(x, 3) for x in m])
+            self.vq, self.vs = zip(*[ots.encode_moments(x, 4, True) for x in root])
+            u8 = lambda l: [torch.from_numpy(t.copy()).to(DEV) for t in l]   # noqa: E731
+            self.md, self.msd, self.vd, self.vsd = u8(self.mq), u8(self.ms), u8(self.vq), u8(self.vs)
+        else:
+            self.m, self.v = m, [r * r for r in root]
+            self.md, self.vd = [_f32(t) for t in self.m], [_f32(t) for t in self.v]
+            self.msd = self.vsd = None
+        self.copies = [torch.zeros(n, dtype=torch.bfloat16, device=DEV) for n in sizes]
+
+    def state(self):
+        return self.pd + self.md + self.vd + (self.msd + self.vsd if self.eight else []) + self.copies
+
+    def call(self, step, copies=True, scale=None, stream=None, **hyper):
+        kw = {**HYPER, **hyper, "copies": self.copies if copies else None, "grad_scale": scale,
+              "stream": stream}
+        if self.eight:
+            fq().adamw_8bit(self.pd, self.gd, self.md, self.msd, self.vd, self.vsd, step, **kw)
+        else:
+            fq().adamw(self.pd, self.gd, self.md, self.vd, step, **kw)
+
+    def check(self, step, copies=True, scale=1.0, **hyper):
+        """The device's state after one call against the host's before it, which
+        then takes the device's."""
+        h = {**HYPER, **hyper}
+        b1, b2 = h["betas"]
+        for i in range(len(self.sizes)):
+            g = self.g[i] * np.float32(scale)
+            if self.eight:
+                m0 = ots.decode_moments(self.mq[i], self.ms[i])
+                r = ots.decode_moments(self.vq[i], self.vs[i])
+                v0 = r * r
+            else:
+                m0, v0 = self.m[i], self.v[i]
+            m, v = ots.adamw_moments(m0, v0, g, b1, b2)
+            p, up = ots.adamw_parameters(self.p[i], m, v, step, h["lr"], b1, b2,
+                                         float(np.float32(h["eps"])), h["weight_decay"])
+            got = host(self.pd[i])
+            tol = 3 * U * np.abs(self.p[i]) + 8 * U * np.abs(up) + U * np.abs(p)
+            bad = ~(np.abs(got - p) <= tol)
+            assert not bad.any(), (i, np.flatnonzero(bad)[:4], got[bad][:4], p[bad][:4])
+            if copies:
+                want = torch.from_numpy(got).to(torch.bfloat16)
+                assert torch.equal(self.copies[i].cpu().view(torch.int16), want.view(torch.int16))
+            if self.eight:
+                for x, second, qd, sd in ((m, False, self.md[i], self.msd[i]),
+                                          (np.sqrt(v), True, self.vd[i], self.vsd[i])):
+                    q, s = ots.encode_moments(x, step, second)
+                    assert np.array_equal(host(qd), q) and np.array_equal(host(sd), s), (i, second)
+            else:
+                assert np.array_equal(host(self.md[i]), m) and np.array_equal(host(self.vd[i]), v), i
+        self.p = [host(t) for t in self.pd]
+        if self.eight:
+            self.mq, self.ms = [host(t) for t in self.md], [host(t) for t in self.msd]
+            self.vq, self.vs = [host(t) for t in self.vd], [host(t) for t in self.vsd]
+        else:
+            self.m, self.v = [host(t) for t in self.md], [host(t) for t in self.vd]
+
+
+SIZES = [1, 2, 3, 4, 5, 63, 64, 65, 66, 67, 68, 69, 127, 128, 129, 131, 191, 192, 193, 255, 256, 257, 511,
+         1000, 2047, 2048, 2049, 4096, 10001]
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("eight", [False, True])
+def test_sizes(eight, grad):
+    """Every size alone and all in one call, three steps each."""
+    for sizes in [[n] for n in SIZES] + [SIZES]:
+        t = Tensors(sizes, eight, grad, seed=len(sizes))
+        for step in (5, 6, 7):
+            t.call(step)
+            t.check(step)
+
+
+@pytest.mark.parametrize("count", [1, 47, 48, 49, 96, 97, 150])
+def test_counts(count):
+    """More tensors than one launch describes, empty ones among them."""
+    sizes = [(37 * i) % 300 if i % 9 else 0 for i in range(count)]
+    for eight in (False, True):
+        t = Tensors(sizes, eight, "bf16", seed=count)
+        t.call(11)
+        t.check(11)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_from_the_first_step(eight):
+    """From zero moments (zero codes and scales) on, with and without copies."""
+    t = Tensors([300, 128, 7], eight, "f32", seed=2, zero=True)
+    for step in (1, 2, 3, 4):
+        t.call(step, copies=step % 2 == 1)
+        t.check(step, copies=step % 2 == 1)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_hyperparameters(eight):
+    for k, h in enumerate([dict(betas=(0.0, 0.95)), dict(betas=(0.9, 0.0)), dict(betas=(0.0, 0.0)),
+                           dict(betas=(0.99, 0.9999)), dict(weight_decay=0.0), dict(lr=0.0),
+                           dict(eps=1e-3), dict(lr=1.0, weight_decay=0.5)]):
+        t = Tensors([515], eight, "f32", seed=k)
+        for step in (1, 1000, 10 ** 6, 2 ** 31 + 7):
+            t.call(step, **h)
+            t.check(step, **h)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_scalars_on_the_device(eight):
+    """Step, rate and gradient scale from the device give what the host's give, to
+    the rounding of lr to FP32 (none here: it is an FP32 value)."""
+    lr = float(np.float32(2e-3))
+    scale = torch.tensor([0.37], device=DEV)
+    a, b = [Tensors([1000, 77], eight, "bf16", seed=9) for _ in range(2)]
+    for step in (1, 2, 700):
+        a.call(step, scale=scale, lr=lr)
+        a.check(step, scale=0.37, lr=lr)
+        b.call(torch.tensor([step], dtype=torch.int32, device=DEV), scale=scale,
+               lr=torch.tensor([lr], device=DEV))
+        for x, y in zip(a.state(), b.state()):
+            assert torch.equal(x, y)
+        b.check(step, scale=0.37, lr=lr)
+    # each alone
+    for kw in (dict(lr=torch.tensor(lr, device=DEV)), dict(lr=lr)):
+        for step in (701, torch.tensor(701, dtype=torch.int32, device=DEV)):
+            c, d = [Tensors([555], eight, "f32", seed=3) for _ in range(2)]
+            c.call(701, lr=lr)
+            d.call(step, **kw)
+            for x, y in zip(c.state(), d.state()):
+                assert torch.equal(x, y)
+
+
+def test_zero_gradients_and_moments_keep_their_zeros():
+    """An element without a gradient ever: its moments stay zero and only the decay
+    moves it (eps keeps the quotient from 0/0); a group of them has scale 0."""
+    for eight in (False, True):
+        t = Tensors([400], eight, "f32", zero=True)
+        t.g[0][:] = 0
+        t.g[0][130] = 1e-3
+        t.gd[0].copy_(_f32(t.g[0]))
+        p = host(t.pd[0]).copy()
+        for step in (1, 2):
+            t.call(step)
+            t.check(step)
+        keep = np.arange(400) != 130
+        want = p * np.float32(1 - 3e-4)
+        assert np.abs(host(t.pd[0])[keep] - (want * np.float32(1 - 3e-4))[keep]).max() < 1e-6
+        assert not t.md[0][:128].any() and not t.vd[0][:128].any()
+        if eight:
+            assert t.msd[0][0] == 0 and t.vsd[0][0] == 0
+
+
+def test_a_root_far_below_its_groups_largest_keeps_a_code():
+    """One element's gradients are 10^7 times the others': their roots are below the
+    smallest code, keep it, and their steps stay bounded."""
+    t = Tensors([128], True, "f32", zero=True)
+    t.g[0][:] = 1e-7
+    t.g[0][5] = 1.0
+    t.gd[0].copy_(_f32(t.g[0]))
+    p = host(t.pd[0]).copy()
+    for step in range(1, 6):
+        t.call(step, weight_decay=0.0)
+        t.check(step, weight_decay=0.0)
+    others = np.arange(128) != 5
+    assert (host(t.vd[0])[others] == 1).all()
+    assert np.abs(host(t.pd[0]) - p).max() <= 5 * HYPER["lr"] * 1.5
+
+
+def test_moments_in_8_bits_reach_a_constant_gradient():
+    """A constant gradient: from 250 steps on every m is one of the two codes around g,
+    and v's root around |g|, within a step of E4M3 (1/8 of a value at most).
+
+    The largest of a group is always code 448, exact but for FP32, so that after 250
+    steps (0.9^250, 0.95^250) the scale stands.  While a code q is more than a step
+    below g, d = |g| - q, the new value is q + (1 - b) d at least (of a root, q + (1 -
+    b2) d to first order), rounded up in steps whose u lies in an interval of length
+    (1 - b) d/step.  Points of N successive multiples of the golden ratio leave no gap
+    of phi^2/N, so one of 2.62 step/((1 - b) d) steps goes up: 27 (1 + 1/2 + 1/3 + ...)
+    steps for m's last codes, 53 (...) for the root's, and the first codes, while the
+    value is far, pass in fewer.  Between the codes around g the new value stays
+    between them.  Rounded to the nearest, m would stop where (1 - b) d is below half
+    a step: 5 steps short.  (That the mean is closer still is not claimed: successive
+    steps' u are related.)"""
+    n = 256
+    t = Tensors([n], True, "f32", zero=True)
+    rng = np.random.default_rng(3)
+    g = (rng.uniform(0.2, 1.0, n) * rng.choice([-1, 1], n)).astype(np.float32)
+    t.gd[0].copy_(_f32(g))
+    for step in range(1, 301):
+        t.call(step, copies=False, lr=0.0, weight_decay=0.0)
+        if step > 250:
+            m = ots.decode_moments(host(t.md[0]), host(t.msd[0]))
+            r = ots.decode_moments(host(t.vd[0]), host(t.vsd[0]))
+            assert np.abs(m / g - 1).max() < 0.125 + 1e-4
+            assert np.abs(r / np.abs(g) - 1).max() < 0.125 + 1e-4
+
+
+def test_shapes_views_and_versions():
+    """Tensors of any shape; views of a flat buffer; autograd hears of the writes."""
+    flat = torch.randn(4096, device=DEV)
+    p = [flat[:1200].view(30, 40), flat[1216:1217].view(()), flat[2048:4096].view(2, 32, 32)]
+    rest = flat.clone()
+    g = [torch.randn(t.shape, device=DEV) for t in p]
+    m, v = [torch.zeros_like(t) for t in p], [torch.zeros_like(t) for t in p]
+    was = [t._version for t in p + m + v]
+    fq().adamw(p, g, m, v, 1)
+    assert all(t._version > w for t, w in zip(p + m + v, was))
+    for lo, hi in ((1200, 1216), (1217, 2048)):
+        assert torch.equal(flat[lo:hi], rest[lo:hi])
+    for h, x in zip(g, m):
+        assert torch.allclose(x, 0.1 * h, rtol=1e-6)
+    w = torch.randn(50, device=DEV, requires_grad=True)
+    loss = (w * w).sum()
+    with torch.no_grad():
+        fq().adamw([w], [torch.ones_like(w)], [torch.zeros_like(w)], [torch.zeros_like(w)], 1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_the_same_parameter_twice_is_refused():
+    t = Tensors([300, 300], False, "f32")
+    t.pd[1] = t.pd[0]
+    before = [x.clone() for x in t.state()]
+    with pytest.raises(fq().Fp8qError):
+        t.call(1)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, t.state()))
+
+
+def test_python_path_gives_the_same():
+    """The compiled call and the wrapper's own path."""
+    for eight in (False, True):
+        a, b = [Tensors([300, 2049], eight, "bf16", seed=5) for _ in range(2)]
+        a.call(3)
+        b.call(3, stream=torch.cuda.current_stream())
+        for x, y in zip(a.state(), b.state()):
+            assert torch.equal(x, y)
+
+
+def test_elements_past_32_bit_offsets():
+    """A tensor of more than 2^32 bytes (2^30 elements and some): its last elements,
+    whose dither goes by their place's low 32 bits."""
+    n = (1 << 30) + 1234
+    p, g = torch.ones(n, device=DEV), torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    groups = -(-n // 128)
+    m, v = [torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    ms, vs = [torch.zeros(groups, device=DEV) for _ in range(2)]
+    tail = 128 * (groups - 5)
+    rng = np.random.default_rng(1)
+    g[tail:] = _f32(rng.standard_normal(n - tail)).to(torch.bfloat16)
+    fq().adamw_8bit([p], [g], [m], [ms], [v], [vs], 1, **HYPER)
+    gt = host(g[tail:].float())
+    z = np.zeros(n - tail, dtype=np.float32)
+    m2, v2 = ots.adamw_moments(z, z, gt, 0.9, 0.95)
+    want, _ = ots.adamw_parameters(z + 1, m2, v2, 1, 3e-3, 0.9, 0.95, float(np.float32(1e-8)), 0.1)
+    assert np.abs(host(p[tail:]) - want).max() <= 8 * U
+    for x, second, q, sc in ((m2, False, m, ms), (np.sqrt(v2), True, v, vs)):
+        codes, scales = ots.encode_moments(x, 1, second, first=tail)
+        assert np.array_equal(host(q[tail:]), codes)
+        assert np.array_equal(host(sc[groups - 5:]), scales)
+    assert not m[:tail].any() and bool((p[:tail] == p[0]).all())
