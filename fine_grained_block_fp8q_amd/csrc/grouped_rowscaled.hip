@@ -9,13 +9,21 @@
 // product of its two scales, as in the dense row-scaled GEMM.
 //
 // An expert has few tokens (128 .. 1024) for a large C, so that the call is bound
-// by writing C: 128 x 128 outputs of 1 .. 8 groups each, read once from L2 and
-// written once.  A workgroup of 4 waves takes such a tile (64 x 64 a wave), two
-// workgroups a CU, so that one's stores go out under the other's products.  The
-// groups come into LDS by direct loads, two stages; rows of 128 bytes with
-// exchanged 16-byte columns (swz), so that fragment reads are free of conflicts.
+// by writing C, and a tile of C has few groups to sum: what costs time is the
+// latency at a tile's start and end.  A persistent workgroup of 4 waves therefore
+// walks tiles of 128 x 128 (64 x 64 a wave) as one stream of groups: the next
+// group's loads, the next tile's first one among them, go out before a group is
+// computed, and a tile's stores drain while the next is summed.  Two workgroups a
+// CU, two stages of one group each in LDS (direct loads; rows of 128 bytes with
+// exchanged 16-byte columns, swz, so that fragment reads are free of conflicts).
 // The product is formed transposed (matrix-core rows are B's rows), so that a
-// lane's four results are consecutive in k.
+// lane's four results are consecutive in k; 16 rows of a wave's part pass through
+// LDS and leave as whole 128-byte lines.
+//
+// Each XCD takes a run of the tiles (all of an expert's follow each other: its
+// operands stay in that XCD's L2), cut so that the runs' groups, plus
+// kTileCost for every tile's stores, are equal; its workgroups take the run's
+// tiles in turn.
 
 #include "experts.hpp"
 #include "fp8q.h"
@@ -24,117 +32,319 @@
 
 namespace fp8q {
 
-constexpr int kWgTile = 128, kWgThreads = 256;
-constexpr int kWgOperand = kWgTile * 128;                   // bytes of one operand's group
-constexpr int kWgStage = 2 * kWgOperand + 2 * kWgTile * 4;  // and both scales'
-constexpr int kWgLoads = 9;  // of one wave and group: 4 + 4 KiB of operands, scales
+// A tile of TN rows of A by TK rows of B, WN x WK waves of 64 x TK/WK each.
+template <int TN_, int TK_, int WN_, int WK_, int PER_CU_>
+struct WgCfg {
+  static constexpr int TN = TN_, TK = TK_, WN = WN_, WK = WK_, PER_CU = PER_CU_;
+  static constexpr int WAVES = WN * WK, THREADS = 64 * WAVES;
+  static constexpr int NJ = TK / WK / 16;                     // blocks of 16 rows of B a wave
+  static constexpr int A_BYTES = TN * 128, B_BYTES = TK * 128;
+  static constexpr int SCALES = A_BYTES + B_BYTES;            // their place in a stage
+  static constexpr int STAGE = SCALES + (TN + TK) * 4;
+  static constexpr int A_LOADS = TN / 8 / WAVES, B_LOADS = TK / 8 / WAVES;  // of 1 KiB, a wave
+  static constexpr int LOADS = A_LOADS + B_LOADS + 1;         // and 64 scales
+  static constexpr int STORES = 4 * NJ / 2;                   // of 1 KiB in BF16, a wave and tile
+  static_assert(TN == 64 * WN && (TN + TK) == 64 * WAVES, "64 rows and 64 scales a wave");
+  static_assert(LOADS + 2 * STORES < 64, "vmcnt range");
+};
+using WgLarge = WgCfg<256, 256, 4, 2, 1>;
+using WgSmall = WgCfg<128, 128, 2, 2, 2>;
+
+constexpr int kWgExperts = 1024;
+constexpr int kRowPitch = 128 + 16;     // bytes of a row on its way out
+constexpr int kLag = 2;                 // blocks between a product and its folding
+constexpr int64_t kLargeTiles = 2;      // of 256 x 256 a CU, from which they are taken
+constexpr int kTileCost = 2;            // a tile's stores, in groups
+
+template <class Cfg>
+struct WgShared {
+  uint8_t stage[2][Cfg::STAGE];
+  uint8_t out[Cfg::WAVES][16 * kRowPitch];
+  int group0[kWgExperts + 1];  // groups before each expert, and all
+};
+static_assert(WgLarge::PER_CU * sizeof(WgShared<WgLarge>) <= 160 * 1024 &&
+                  WgSmall::PER_CU * sizeof(WgShared<WgSmall>) <= 160 * 1024,
+              "the workgroups of a CU fit its LDS");
+
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+// A wave's 16 rows through its place in LDS: four pieces of 8 bytes (32 apart), or
+// two of 16 (64 apart), written at `w`, 16 bytes read back at `r` and 8 rows further
+// on (a wave's LDS accesses are served in order).  By the compiler's own accesses
+// they would first wait for every direct load in flight, which it takes to write
+// anywhere in LDS.
+__device__ __forceinline__ void through_lds(uint32_t w, uint32_t r, const v2u (&p)[4], v4u& lo,
+                                            v4u& hi) {
+  asm volatile(
+      "ds_write_b64 %2, %4\n\tds_write_b64 %2, %5 offset:32\n\tds_write_b64 %2, %6 offset:64\n\t"
+      "ds_write_b64 %2, %7 offset:96\n\t"
+      "ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(lo), "=&v"(hi)
+      : "v"(w), "v"(r), "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "n"(8 * kRowPitch)
+      : "memory");
+}
+__device__ __forceinline__ void through_lds(uint32_t w, uint32_t r, const v4f& p0, const v4f& p1,
+                                            v4u& lo, v4u& hi) {
+  asm volatile(
+      "ds_write_b128 %2, %4\n\tds_write_b128 %2, %5 offset:64\n\t"
+      "ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(lo), "=&v"(hi)
+      : "v"(w), "v"(r), "v"(p0), "v"(p1), "n"(8 * kRowPitch)
+      : "memory");
+}
+
+// The experts' first groups into `group0`; false where off is invalid.  Every wave
+// finds the same; the first writes.
+__device__ __forceinline__ bool expert_prefix(const int32_t* off, int G, int64_t most, int* group0) {
+  const int lane = threadIdx.x & 63, PL = (G + 63) >> 6, e0 = lane * PL;
+  int sum = 0;
+  bool bad = lane == 0 && off[0] != 0;
+  for (int i = 0; i < PL; ++i)
+    if (e0 + i < G) {
+      const int lo = off[e0 + i], hi = off[e0 + i + 1];
+      bad = bad || hi < lo;
+      sum += groups_of(hi - lo);
+    }
+  if (__ballot(bad) != 0) return false;
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(inc, d);
+    if (lane >= d) inc += v;
+  }
+  if ((int64_t)__builtin_amdgcn_readlane(inc, 63) > most) return false;
+  if (threadIdx.x < 64) {
+    int at = inc - sum;
+    if (lane == 0) group0[0] = 0;
+    for (int i = 0; i < PL; ++i)
+      if (e0 + i < G) {
+        at += groups_of(off[e0 + i + 1] - off[e0 + i]);
+        group0[e0 + i + 1] = at;
+      }
+  }
+  return true;
+}
+
+// First tile of share x of `shares` equal ones, by cost: tiles * (groups + kTileCost)
+// an expert.
+__device__ __forceinline__ int share_start(const int* group0, int G, int tiles, int x, int shares) {
+  auto cost = [&](int e) { return (int64_t)tiles * (group0[e] + (int64_t)kTileCost * e); };
+  const int64_t want = cost(G) * x / shares;
+  int lo = 0, hi = G;  // cost(lo) <= want < cost(hi), or want is the end
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cost(mid) <= want) lo = mid; else hi = mid;
+  }
+  const int each = group0[lo + 1] - group0[lo] + kTileCost;
+  const int64_t in = (want - cost(lo)) / each;
+  return lo * tiles + (int)(in < tiles ? in : tiles);
+}
+
+// A fragment's two 16-byte pieces.
+__device__ __forceinline__ v8i frag_at(const uint8_t* lo, const uint8_t* hi, int at) {
+  const v4i l = *reinterpret_cast<const v4i*>(lo + at), h = *reinterpret_cast<const v4i*>(hi + at);
+  return v8i{l[0], l[1], l[2], l[3], h[0], h[1], h[2], h[3]};
+}
 
 // PRECISE: each P_g by FP16 matrix-core instructions on the codes widened to FP16.
-template <bool PRECISE>
-__global__ __launch_bounds__(kWgThreads, 2) void grouped_rowscaled_kernel(
-    const uint8_t* __restrict__ A, const float* __restrict__ SA, const uint8_t* __restrict__ B,
-    const float* __restrict__ SB, const int32_t* __restrict__ off, int G, int64_t T, int64_t N,
-    int64_t K, void* __restrict__ C, int out_bf16, int tiles_k, int tiles) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kWgStage];
-  const int e = (int)(blockIdx.x / tiles), tile = (int)(blockIdx.x % tiles);
-  const ExpertSpan span = expert_span<false>(off, G, 0x7FFFFFFF, T / 128, e);
-  if (invalid(span)) return;
-  const int groups = groups_of(span.rows);
-  const int64_t n0 = (int64_t)(tile / tiles_k) * kWgTile, k0 = (int64_t)(tile % tiles_k) * kWgTile;
+template <class Cfg, bool PRECISE, bool OUT_BF16>
+__device__ __forceinline__ void grouped_rowscaled(
+    const uint8_t* A, const float* SA, const uint8_t* B, const float* SB, const int32_t* off, int G,
+    int64_t T, int N, int K, void* C, int tiles_k, int tiles, WgShared<Cfg>& sh) {
+  constexpr int NJ = Cfg::NJ, W = Cfg::WAVES;
+  if (!expert_prefix(off, G, T / 128, sh.group0)) {
+#ifdef FP8Q_DEBUG_CHECKS
+    if (blockIdx.x == 0 && threadIdx.x == 0) g_experts_error = 1;
+#endif
+    return;
+  }
+  __syncthreads();
+  const int x = blockIdx.x % kXcds, step = gridDim.x / kXcds;
+  const int first = __builtin_amdgcn_readfirstlane(share_start(sh.group0, G, tiles, x, kXcds)) +
+                    (int)(blockIdx.x / kXcds);
+  const int end = __builtin_amdgcn_readfirstlane(share_start(sh.group0, G, tiles, x + 1, kXcds));
+
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = wave >> 1, wk = wave & 1;
+  const int wn = wave / Cfg::WK, wk = wave % Cfg::WK;
   const int r16 = lane & 15, q = lane >> 4;
 
-  v4f acc[4][4];  // [16 rows of A][16 rows of B]
+  // Operand loads: instruction m of an operand carries rows 8m .. 8m+7, lane l to LDS
+  // byte 16 l: row l/8, physical column l%8.  (Rows past the operand's last are out
+  // of its range: zeros.)
+  uint32_t voff[Cfg::A_LOADS > Cfg::B_LOADS ? Cfg::A_LOADS : Cfg::B_LOADS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
-  // Operand loads: instruction m (0 .. 15) of an operand carries rows 8m .. 8m+7,
-  // lane l to LDS byte 16 l: row l/8, physical column l%8.
-  const int64_t t0 = (int64_t)span.group0 * 128;
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(A + n0 * T + t0, kWgTile * T - t0);
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + k0 * T + t0, kWgTile * T - t0);
-  uint32_t voff[4];
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const int r = (d * 4 + wave) * 8 + (lane >> 3);
+  for (int d = 0; d < (int)(sizeof voff / sizeof voff[0]); ++d) {
+    const int r = (d * W + wave) * 8 + (lane >> 3);
     voff[d] = (uint32_t)(r * T) + (uint32_t)(swz(r, lane & 7) * 16);
   }
-  // Scales: waves 0, 1 the 128 of A, waves 2, 3 those of B.
-  const bool s_a = wave < 2;
-  const float* sbase = (s_a ? SA + span.group0 * N + n0 : SB + span.group0 * K + k0) + (wave & 1) * 64;
-  const int64_t s_ld = s_a ? N : K;
 
-  auto issue = [&](int g) {
-    uint8_t* const st = smem + (g & 1) * kWgStage;
+  // The stream's place: tile `lt`, group `lg` of its expert's `ln` from `lg0` on.
+  int lt = first, lg = 0, ln = 0;
+  __amdgpu_buffer_rsrc_t ra, rb;
+  const float* sbase = nullptr;
+  int s_ld = 0, s_bytes = 0;
+  auto enter = [&] {  // the first tile from lt on that has groups
+    for (; lt < end; lt += step) {
+      const int e = lt / tiles, in = lt - e * tiles;
+      const int g0 = __builtin_amdgcn_readfirstlane(sh.group0[e]);
+      ln = __builtin_amdgcn_readfirstlane(sh.group0[e + 1]) - g0;
+      if (ln == 0) continue;
+      const int tn = in / tiles_k, n0 = tn * Cfg::TN, k0 = (in - tn * tiles_k) * Cfg::TK;
+      const int64_t t0 = (int64_t)g0 * 128;
+      const int na = N - n0 < Cfg::TN ? N - n0 : Cfg::TN, nb = K - k0 < Cfg::TK ? K - k0 : Cfg::TK;
+      ra = make_rsrc(A + n0 * T + t0, na * T - t0);
+      rb = make_rsrc(B + k0 * T + t0, nb * T - t0);
+      // Scales: the first TN/64 waves those of A, the others those of B, 64 each.
+      const bool s_a = wave < Cfg::TN / 64;
+      const int at = (s_a ? wave : wave - Cfg::TN / 64) * 64, live = (s_a ? na : nb) - at;
+      s_ld = s_a ? N : K;
+      s_bytes = live < 64 ? (live > 0 ? live * 4 : 0) : 256;
+      sbase = (s_a ? SA + n0 : SB + k0) + (int64_t)g0 * s_ld + at;
+      lg = 0;
+      return;
+    }
+  };
+  // The stream's next group into stage `at`, if there is one.
+  auto issue = [&](int at) {
+    if (lt >= end) return false;
+    uint8_t* const st = sh.stage[at];
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to_lds(st + (d * 4 + wave) * 1024), 16, voff[d],
-                                               g * 128, 0, 0);
+    for (int d = 0; d < Cfg::A_LOADS; ++d)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to_lds(st + (d * W + wave) * 1024), 16, voff[d],
+                                               lg * 128, 0, 0);
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to_lds(st + kWgOperand + (d * 4 + wave) * 1024),
-                                               16, voff[d], g * 128, 0, 0);
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(sbase + g * s_ld, 256);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to_lds(st + 2 * kWgOperand + wave * 256), 4,
+    for (int d = 0; d < Cfg::B_LOADS; ++d)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to_lds(st + Cfg::A_BYTES + (d * W + wave) * 1024),
+                                               16, voff[d], lg * 128, 0, 0);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(sbase + (int64_t)lg * s_ld, s_bytes);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to_lds(st + Cfg::SCALES + wave * 256), 4,
                                              (uint32_t)(lane * 4), 0, 0, 0);
+    if (++lg == ln) {
+      lt += step;
+      enter();
+    }
+    return true;
   };
 
-  if (groups > 0) issue(0);
-  for (int g = 0; g < groups; ++g) {
-    if (g + 1 < groups) {
-      issue(g + 1);
-      wait_vmcnt<kWgLoads>();
-    } else {
-      wait_vmcnt<0>();
-    }
-    lds_barrier();
-    const uint8_t* const st = smem + (g & 1) * kWgStage;
-    const float* const sa_s = reinterpret_cast<const float*>(st + 2 * kWgOperand);
-    v8i a[4];
-    float sa[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = load_frag(st, wn * 64 + i * 16 + r16, q);
-      sa[i] = sa_s[wn * 64 + i * 16 + r16];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const v8i b = load_frag(st + kWgOperand, wk * 64 + j * 16 + r16, q);
-      const v4f sb = *reinterpret_cast<const v4f*>(sa_s + 128 + wk * 64 + j * 16 + 4 * q);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v4f p = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (PRECISE) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            p = mfma_wide16(widen_quarter(b, h), widen_quarter(a[i], h), p);
-        } else {
-          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a[i], p, 0, 0, 0, 0, 0, 0);
-        }
-        promote_rows(acc[i][j], p, sa[i], sb);
-      }
-    }
-    lds_barrier();  // the stage is free
-  }
+  // This lane's places in a stage: its row of a block of 16 and the pieces q and q+4
+  // of the row (the exchange of columns goes by the row in its block).
+  const int f_lo = r16 * 128 + swz(r16, q) * 16, f_hi = r16 * 128 + swz(r16, q + 4) * 16;
+  const int fa = wn * 64 * 128, fb = Cfg::A_BYTES + wk * NJ * 16 * 128;
+  const int fsa = Cfg::SCALES + (wn * 64 + r16) * 4;
+  const int fsb = Cfg::SCALES + (Cfg::TN + wk * NJ * 16 + 4 * q) * 4;
 
-  // Block (i, j): the lane holds n = 16 i + r16, k = 16 j + 4 q .. +3.
-  const int64_t c0 = ((int64_t)e * N + n0 + wn * 64) * K + k0 + wk * 64;
+  constexpr int OB = OUT_BF16 ? 2 : 4, JS = OUT_BF16 ? 4 : 2;  // blocks of 128 bytes
+  constexpr int kStores = Cfg::STORES * OB / 2;
+  const uint32_t mine = (uint32_t)(uintptr_t)to_lds(sh.out[wave]);
+  const uint32_t out_w = mine + r16 * kRowPitch + 4 * q * OB;
+  const uint32_t out_r = mine + (lane >> 3) * kRowPitch + 16 * (lane & 7);
+
+  enter();
+  issue(0);
+  int cur = 0;
+  bool stored = false;  // the stores of the tile before are behind the loads in flight
+  for (int t = first; t < end; t += step) {
+    const int e = t / tiles, in = t - e * tiles, tn = in / tiles_k;
+    const int n0 = tn * Cfg::TN + wn * 64, k0 = (in - tn * tiles_k) * Cfg::TK + wk * NJ * 16;
+    const bool live = n0 < N && k0 < K;
+    const int groups = __builtin_amdgcn_readfirstlane(sh.group0[e + 1] - sh.group0[e]);
+    v4f acc[4][NJ];  // [16 rows of A][16 rows of B]
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t at = c0 + (int64_t)(i * 16 + r16) * K + j * 16 + 4 * q;
-      if (out_bf16)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(C) + at) =
-            make_uint2(f32_to_bf16_bits(acc[i][j][0]) | (f32_to_bf16_bits(acc[i][j][1]) << 16),
-                       f32_to_bf16_bits(acc[i][j][2]) | (f32_to_bf16_bits(acc[i][j][3]) << 16));
-      else
-        *reinterpret_cast<v4f*>(static_cast<float*>(C) + at) = acc[i][j];
+      for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < groups; ++g) {
+      // This group's loads came before the last tile's stores and the next group's.
+      const bool more = issue(cur ^ 1);
+      if (more) {
+        if (stored) wait_vmcnt<Cfg::LOADS + kStores>(); else wait_vmcnt<Cfg::LOADS>();
+      } else {
+        if (stored) wait_vmcnt<kStores>(); else wait_vmcnt<0>();
+      }
+      stored = false;
+      lds_barrier();
+      if (live) {
+        const uint8_t* const st = sh.stage[cur];
+        const uint8_t *const a_lo = st + fa + f_lo, *const a_hi = st + fa + f_hi;
+        const uint8_t *const b_lo = st + fb + f_lo, *const b_hi = st + fb + f_hi;
+        const uint8_t *const s_a = st + fsa, *const s_b = st + fsb;
+        v8i a[4], b[2];
+        float sa[4];
+        v4f sb[3], p[kLag + 1];
+        auto row_block = [&](int j) {
+          b[j % 2] = frag_at(b_lo, b_hi, j * 2048);
+          sb[j % 3] = *reinterpret_cast<const v4f*>(s_b + j * 64);
+        };
+        row_block(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = frag_at(a_lo, a_hi, i * 2048);
+          sa[i] = *reinterpret_cast<const float*>(s_a + i * 64);
+        }
+        // Block k = 4 j + i is folded kLag blocks later, when the matrix core has
+        // written it (held in this order: the compiler would fold it at once, and wait).
+#pragma unroll
+        for (int k = 0; k < 4 * NJ + kLag; ++k) {
+          const int i = k % 4, j = k / 4;
+          if (k < 4 * NJ) {
+            if (i == 0 && j < NJ - 1) row_block(j + 1);
+            v4f& o = p[k % (kLag + 1)];
+            o = v4f{0.f, 0.f, 0.f, 0.f};
+            if constexpr (PRECISE) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                o = mfma_wide16(widen_quarter(b[j % 2], h), widen_quarter(a[i], h), o);
+            } else {
+              o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j % 2], a[i], o, 0, 0, 0, 0, 0, 0);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (k >= kLag) {
+            const int d = k - kLag;
+            promote_rows(acc[d % 4][d / 4], p[d % (kLag + 1)], sa[d % 4], sb[d / 4 % 3]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      lds_barrier();  // the stage is free
+      cur ^= 1;
     }
+
+    // Block (i, j): the lane holds n = 16 i + r16, k = 16 j + 4 q .. +3.
+    stored = live;
+    if (!live) continue;
+    uint8_t* const c0 = static_cast<uint8_t*>(C) +
+                        (((int64_t)e * N + n0 + (lane >> 3)) * K + k0) * OB + 16 * (lane & 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j0 = 0; j0 < NJ; j0 += JS) {
+        v4u lo, hi;
+        if constexpr (OUT_BF16) {
+          v2u p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            p[j] = v2u{pack_bf16x2(acc[i][j0 + j][0], acc[i][j0 + j][1]),
+                       pack_bf16x2(acc[i][j0 + j][2], acc[i][j0 + j][3])};
+          through_lds(out_w, out_r, p, lo, hi);
+        } else {
+          through_lds(out_w, out_r, acc[i][j0], acc[i][j0 + 1], lo, hi);
+        }
+        uint8_t* const to = c0 + ((int64_t)(16 * i) * K + 16 * j0) * OB;
+        __builtin_nontemporal_store(lo, reinterpret_cast<v4u*>(to));
+        __builtin_nontemporal_store(hi, reinterpret_cast<v4u*>(to + 8 * (int64_t)K * OB));
+      }
+  }
+}
+
+template <class Cfg, bool PRECISE, bool OUT_BF16>
+__global__ __launch_bounds__(Cfg::THREADS, 2) void grouped_rowscaled_kernel(
+    const uint8_t* __restrict__ A, const float* __restrict__ SA, const uint8_t* __restrict__ B,
+    const float* __restrict__ SB, const int32_t* __restrict__ off, int G, int64_t T, int N, int K,
+    void* __restrict__ C, int tiles_k, int tiles) {
+  __shared__ __attribute__((aligned(16))) WgShared<Cfg> sh;
+  grouped_rowscaled<Cfg, PRECISE, OUT_BF16>(A, SA, B, SB, off, G, T, N, K, C, tiles_k, tiles, sh);
 }
 
 #ifdef FP8Q_DEBUG_CHECKS
@@ -143,17 +353,39 @@ hipError_t wgrad_offsets_error_take(hipStream_t stream, int* flag) {
 }
 #endif
 
+template <class Cfg>
+static hipError_t launch(const uint8_t* a_q, const float* a_s, const uint8_t* b_q, const float* b_s,
+                         int64_t T, const int32_t* off, int G, int64_t N, int64_t K, void* c,
+                         int out_bf16, int precise, int cus, hipStream_t stream) {
+  const int64_t tiles_k = (K + Cfg::TK - 1) / Cfg::TK, tiles = (N + Cfg::TN - 1) / Cfg::TN * tiles_k;
+  // (tile numbers, rows and columns are ints)
+  if (tiles > 0x7FFFFFFF / (G + 1) - 1024 || N > 0x7FFFFF00 || K > 0x7FFFFF00)
+    return hipErrorInvalidValue;
+  int64_t grid = (int64_t)cus * Cfg::PER_CU;
+  if (grid > tiles * G) grid = tiles * G;
+  grid = (grid + kXcds - 1) / kXcds * kXcds;
+  auto kern = precise ? (out_bf16 ? grouped_rowscaled_kernel<Cfg, true, true>
+                                  : grouped_rowscaled_kernel<Cfg, true, false>)
+                      : (out_bf16 ? grouped_rowscaled_kernel<Cfg, false, true>
+                                  : grouped_rowscaled_kernel<Cfg, false, false>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::THREADS), 0, stream, a_q, a_s, b_q, b_s,
+                     off, G, T, (int)N, (int)K, c, (int)tiles_k, (int)tiles);
+  return hipGetLastError();
+}
+
 hipError_t launch_grouped_gemm_rowscaled(const uint8_t* a_q, const float* a_s, const uint8_t* b_q,
                                          const float* b_s, int64_t T, const int32_t* off, int G,
                                          int64_t N, int64_t K, void* c, int out_bf16, int precise,
                                          hipStream_t stream) {
   if (N == 0 || K == 0) return hipSuccess;
-  const int64_t tiles_k = K / kWgTile, tiles = N / kWgTile * tiles_k;
-  if (tiles > max_blocks(kWgThreads) / G) return hipErrorInvalidValue;
-  auto kern = precise ? grouped_rowscaled_kernel<true> : grouped_rowscaled_kernel<false>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * G)), dim3(kWgThreads), 0, stream, a_q, a_s, b_q,
-                     b_s, off, G, T, N, K, c, out_bf16, (int)tiles_k, (int)tiles);
-  return hipGetLastError();
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+    return hipGetLastError();
+  const int64_t large = (N + 255) / 256 * ((K + 255) / 256) * G;
+  if (large >= kLargeTiles * cus)
+    return launch<WgLarge>(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, precise, cus, stream);
+  return launch<WgSmall>(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, precise, cus, stream);
 }
 
 }  // namespace fp8q
