@@ -640,8 +640,9 @@ static fp8q_status grouped_rowscaled_call(const uint8_t* a_q, const float* a_s,
       !aligned(b_s, 4) || !aligned(off, 4))
     return FP8Q_ERR_ALIGN;
   if (!valid_out(out)) return FP8Q_ERR_ENUM;
-  // 32-bit offsets within a tile's rows of T bytes
-  if (G > 1024 || T > (int64_t(1) << 24)) return FP8Q_ERR_UNSUPPORTED;
+  // 32-bit offsets within a tile's rows of T bytes, and of 4 K bytes
+  if (G > 1024 || T > (int64_t(1) << 24) || N > (int64_t(1) << 22) || K > (int64_t(1) << 22))
+    return FP8Q_ERR_UNSUPPORTED;
   if (empty_out) return FP8Q_OK;
   const fp8q_status d = check_device();
   if (d != FP8Q_OK) return d;

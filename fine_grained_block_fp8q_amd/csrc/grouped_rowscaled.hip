@@ -17,8 +17,9 @@
 // CU, two stages of one group each in LDS (direct loads; rows of 128 bytes with
 // exchanged 16-byte columns, swz, so that fragment reads are free of conflicts).
 // The product is formed transposed (matrix-core rows are B's rows), so that a
-// lane's four results are consecutive in k; 16 rows of a wave's part pass through
-// LDS and leave as whole 128-byte lines.
+// lane's four results are consecutive in k; the lanes of two rows exchange theirs in
+// registers, so that 8 lanes store a row's 128 consecutive bytes at once (4 lanes and
+// 64 bytes: 622 us where this takes 4xx; through LDS: 517).
 //
 // Each XCD takes a run of the tiles (all of an expert's follow each other: its
 // operands stay in that XCD's L2), cut so that the runs' groups, plus
@@ -51,7 +52,7 @@ using WgLarge = WgCfg<256, 256, 4, 2, 1>;
 using WgSmall = WgCfg<128, 128, 2, 2, 2>;
 
 constexpr int kWgExperts = 1024;
-constexpr int kRowPitch = 128 + 16;     // bytes of a row on its way out
+constexpr int kNonTemporal = 2;         // cache policy bit of a buffer store
 constexpr int kLag = 2;                 // blocks between a product and its folding
 constexpr int64_t kLargeTiles = 2;      // of 256 x 256 a CU, from which they are taken
 constexpr int kTileCost = 2;            // a tile's stores, in groups
@@ -59,38 +60,44 @@ constexpr int kTileCost = 2;            // a tile's stores, in groups
 template <class Cfg>
 struct WgShared {
   uint8_t stage[2][Cfg::STAGE];
-  uint8_t out[Cfg::WAVES][16 * kRowPitch];
   int group0[kWgExperts + 1];  // groups before each expert, and all
 };
 static_assert(WgLarge::PER_CU * sizeof(WgShared<WgLarge>) <= 160 * 1024 &&
                   WgSmall::PER_CU * sizeof(WgShared<WgSmall>) <= 160 * 1024,
               "the workgroups of a CU fit its LDS");
 
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-
-// A wave's 16 rows through its place in LDS: four pieces of 8 bytes (32 apart), or
-// two of 16 (64 apart), written at `w`, 16 bytes read back at `r` and 8 rows further
-// on (a wave's LDS accesses are served in order).  By the compiler's own accesses
-// they would first wait for every direct load in flight, which it takes to write
-// anywhere in LDS.
-__device__ __forceinline__ void through_lds(uint32_t w, uint32_t r, const v2u (&p)[4], v4u& lo,
-                                            v4u& hi) {
-  asm volatile(
-      "ds_write_b64 %2, %4\n\tds_write_b64 %2, %5 offset:32\n\tds_write_b64 %2, %6 offset:64\n\t"
-      "ds_write_b64 %2, %7 offset:96\n\t"
-      "ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:%8\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(lo), "=&v"(hi)
-      : "v"(w), "v"(r), "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "n"(8 * kRowPitch)
-      : "memory");
+// Rows r16 = 2h and 2h + 1 exchange 16-byte pieces: of the even lane's x, y and the odd
+// one's, x becomes the even row's x and y, y the odd row's.
+__device__ __forceinline__ void pair_rows(v4u& x, v4u& y, bool odd) {
+  auto other = [](uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppQuadXor1, 0xF, 0xF, false);
+  };
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t xo = other(x[w]), yo = other(y[w]);
+    x[w] = odd ? yo : x[w];
+    y[w] = odd ? y[w] : xo;
+  }
 }
-__device__ __forceinline__ void through_lds(uint32_t w, uint32_t r, const v4f& p0, const v4f& p1,
-                                            v4u& lo, v4u& hi) {
+
+// The rows of B that block j's matrix-core rows are: row rho = 4 q + r of blocks 2h and
+// 2h + 1 is row 32 h + 8 q + r, and 4 more for the second, so that a lane's results of
+// the two are 8 consecutive k.  Where row r of B keeps its 16-byte column c in LDS: by
+// its place among the 16 rows of a fragment read, as swz does for A.
+__device__ __forceinline__ int b_row(int rho) { return 8 * (rho >> 2) + (rho & 3); }
+__device__ __forceinline__ int b_swz(int r, int c) { return swz(4 * ((r >> 3) & 3) + (r & 3), c); }
+
+// Waits until at most STORES vector memory operations are outstanding (`stored`), or
+// none.  (The choice is within the instructions here: a branch of the compiler's
+// would cut a step in two.)
+template <int STORES>
+__device__ __forceinline__ void wait_loads(int stored) {
   asm volatile(
-      "ds_write_b128 %2, %4\n\tds_write_b128 %2, %5 offset:64\n\t"
-      "ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:%6\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(lo), "=&v"(hi)
-      : "v"(w), "v"(r), "v"(p0), "v"(p1), "n"(8 * kRowPitch)
-      : "memory");
+      "s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lnone%=\n\ts_waitcnt vmcnt(%1)\n\ts_branch .Ldone%=\n"
+      ".Lnone%=:\n\ts_waitcnt vmcnt(0)\n.Ldone%=:"
+      :
+      : "s"(stored), "n"(STORES)
+      : "memory", "scc");
 }
 
 // The experts' first groups into `group0`; false where off is invalid.  Every wave
@@ -172,16 +179,20 @@ __device__ __forceinline__ void grouped_rowscaled(
   // Operand loads: instruction m of an operand carries rows 8m .. 8m+7, lane l to LDS
   // byte 16 l: row l/8, physical column l%8.  (Rows past the operand's last are out
   // of its range: zeros.)
-  uint32_t voff[Cfg::A_LOADS > Cfg::B_LOADS ? Cfg::A_LOADS : Cfg::B_LOADS];
+  static_assert(Cfg::A_LOADS == Cfg::B_LOADS, "as many rows of both");
+  uint32_t voff_a[Cfg::A_LOADS], voff_b[Cfg::B_LOADS];
 #pragma unroll
-  for (int d = 0; d < (int)(sizeof voff / sizeof voff[0]); ++d) {
+  for (int d = 0; d < Cfg::A_LOADS; ++d) {
     const int r = (d * W + wave) * 8 + (lane >> 3);
-    voff[d] = (uint32_t)(r * T) + (uint32_t)(swz(r, lane & 7) * 16);
+    voff_a[d] = (uint32_t)(r * T) + (uint32_t)(swz(r, lane & 7) * 16);
+    voff_b[d] = (uint32_t)(r * T) + (uint32_t)(b_swz(r, lane & 7) * 16);
   }
 
-  // The stream's place: tile `lt`, group `lg` of its expert's `ln` from `lg0` on.
+  // The stream's next group: tile `lt`, group `lg` of its expert's `ln`.  Past the
+  // last one its loads are of nothing (resources of no bytes), so that every step
+  // has as many.
   int lt = first, lg = 0, ln = 0;
-  __amdgpu_buffer_rsrc_t ra, rb;
+  __amdgpu_buffer_rsrc_t ra = make_rsrc(A, 0), rb = ra, rs = ra;
   const float* sbase = nullptr;
   int s_ld = 0, s_bytes = 0;
   auto enter = [&] {  // the first tile from lt on that has groups
@@ -201,141 +212,176 @@ __device__ __forceinline__ void grouped_rowscaled(
       s_ld = s_a ? N : K;
       s_bytes = live < 64 ? (live > 0 ? live * 4 : 0) : 256;
       sbase = (s_a ? SA + n0 : SB + k0) + (int64_t)g0 * s_ld + at;
-      lg = 0;
+      lg = -1;
       return;
     }
+    ra = rb = rs = make_rsrc(A, 0);
   };
-  // The stream's next group into stage `at`, if there is one.
+  // To the next group; before the first, to that.
+  auto advance = [&] {
+    if (lt < end && lg + 1 == ln) {
+      lt += step;
+      enter();
+    }
+    if (lt < end) {
+      ++lg;
+      rs = make_rsrc(sbase + (int64_t)lg * s_ld, s_bytes);
+    }
+  };
   auto issue = [&](int at) {
-    if (lt >= end) return false;
     uint8_t* const st = sh.stage[at];
 #pragma unroll
     for (int d = 0; d < Cfg::A_LOADS; ++d)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to_lds(st + (d * W + wave) * 1024), 16, voff[d],
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to_lds(st + (d * W + wave) * 1024), 16, voff_a[d],
                                                lg * 128, 0, 0);
 #pragma unroll
     for (int d = 0; d < Cfg::B_LOADS; ++d)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to_lds(st + Cfg::A_BYTES + (d * W + wave) * 1024),
-                                               16, voff[d], lg * 128, 0, 0);
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(sbase + (int64_t)lg * s_ld, s_bytes);
+                                               16, voff_b[d], lg * 128, 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to_lds(st + Cfg::SCALES + wave * 256), 4,
                                              (uint32_t)(lane * 4), 0, 0, 0);
-    if (++lg == ln) {
-      lt += step;
-      enter();
-    }
-    return true;
   };
 
   // This lane's places in a stage: its row of a block of 16 and the pieces q and q+4
   // of the row (the exchange of columns goes by the row in its block).
-  const int f_lo = r16 * 128 + swz(r16, q) * 16, f_hi = r16 * 128 + swz(r16, q + 4) * 16;
+  const int c_lo = swz(r16, q) * 16, c_hi = swz(r16, q + 4) * 16;
+  const int a_lo = r16 * 128 + c_lo, a_hi = r16 * 128 + c_hi;
+  const int b_lo = b_row(r16) * 128 + c_lo, b_hi = b_row(r16) * 128 + c_hi;
   const int fa = wn * 64 * 128, fb = Cfg::A_BYTES + wk * NJ * 16 * 128;
   const int fsa = Cfg::SCALES + (wn * 64 + r16) * 4;
-  const int fsb = Cfg::SCALES + (Cfg::TN + wk * NJ * 16 + 4 * q) * 4;
+  const int fsb = Cfg::SCALES + (Cfg::TN + wk * NJ * 16 + 8 * q) * 4;
 
-  constexpr int OB = OUT_BF16 ? 2 : 4, JS = OUT_BF16 ? 4 : 2;  // blocks of 128 bytes
+  constexpr int OB = OUT_BF16 ? 2 : 4;
   constexpr int kStores = Cfg::STORES * OB / 2;
-  const uint32_t mine = (uint32_t)(uintptr_t)to_lds(sh.out[wave]);
-  const uint32_t out_w = mine + r16 * kRowPitch + 4 * q * OB;
-  const uint32_t out_r = mine + (lane >> 3) * kRowPitch + 16 * (lane & 7);
+  const bool odd = r16 & 1;
+  const uint32_t out_to =
+      (uint32_t)((r16 - odd) * K * OB + (OUT_BF16 ? odd * 64 + 16 * q : odd * 16 + 32 * q));
+
+  // What a step has in registers when it begins: its group's fragments of A, the
+  // first of B, and their scales.
+  v8i a[4], b[2];
+  float sa[4], sa_next[4];
+  v4f sb[3], sb_next;
+  auto row_block = [&](const uint8_t* st, int j, v8i& f, v4f& s) {
+    const int row = j / 2 * 32 + j % 2 * 4;
+    f = frag_at(st + fb + b_lo, st + fb + b_hi, row * 128);
+    s = *reinterpret_cast<const v4f*>(st + fsb + row * 4);
+  };
+  auto row_a = [&](const uint8_t* st, int i) {
+    a[i] = frag_at(st + fa + a_lo, st + fa + a_hi, i * 2048);
+    sa_next[i] = *reinterpret_cast<const float*>(st + fsa + i * 64);
+  };
 
   enter();
+  advance();
   issue(0);
+  advance();
+  issue(1);
+  wait_vmcnt<Cfg::LOADS>();
+  lds_barrier();
+  row_block(sh.stage[0], 0, b[0], sb[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    row_a(sh.stage[0], i);
+    sa[i] = sa_next[i];
+  }
   int cur = 0;
-  bool stored = false;  // the stores of the tile before are behind the loads in flight
+  int stored = 0;  // the stores of the tile before are behind the loads in flight
   for (int t = first; t < end; t += step) {
     const int e = t / tiles, in = t - e * tiles, tn = in / tiles_k;
     const int n0 = tn * Cfg::TN + wn * 64, k0 = (in - tn * tiles_k) * Cfg::TK + wk * NJ * 16;
     const bool live = n0 < N && k0 < K;
     const int groups = __builtin_amdgcn_readfirstlane(sh.group0[e + 1] - sh.group0[e]);
     v4f acc[4][NJ];  // [16 rows of A][16 rows of B]
+    auto group = [&](auto first_c) {
+      constexpr bool FIRST = decltype(first_c)::value;
+      // One group.  Block k = 4 j + i is folded kLag blocks later, when the matrix core
+      // has written it (held in this order: the compiler would fold it at once, and
+      // wait).  Before the last row of blocks every fragment of the stage is in
+      // registers: the barrier there frees it for the group after the next, whose
+      // loads go out at once (ahead of a tile's stores, so that they are waited for
+      // without them), and makes the next group's fragments readable, which take the
+      // places of those that have served.
+      constexpr int kBar = 4 * (NJ - 1) - 2, kLast = 4 * (NJ - 1);
+      const uint8_t *const st = sh.stage[cur], *const st_next = sh.stage[cur ^ 1];
+      v4f p[kLag + 1];
+      advance();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int k = 0; k < 4 * NJ + kLag; ++k) {
+        const int i = k % 4, j = k / 4;
+        if (k < 4 * NJ) {
+          if (i == 0 && j < NJ - 1) row_block(st, j + 1, b[(j + 1) % 2], sb[(j + 1) % 3]);
+          v4f& o = p[k % (kLag + 1)];
+          o = v4f{0.f, 0.f, 0.f, 0.f};
+          if constexpr (PRECISE) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int g = 0; g < groups; ++g) {
-      // This group's loads came before the last tile's stores and the next group's.
-      const bool more = issue(cur ^ 1);
-      if (more) {
-        if (stored) wait_vmcnt<Cfg::LOADS + kStores>(); else wait_vmcnt<Cfg::LOADS>();
-      } else {
-        if (stored) wait_vmcnt<kStores>(); else wait_vmcnt<0>();
-      }
-      stored = false;
-      lds_barrier();
-      if (live) {
-        const uint8_t* const st = sh.stage[cur];
-        const uint8_t *const a_lo = st + fa + f_lo, *const a_hi = st + fa + f_hi;
-        const uint8_t *const b_lo = st + fb + f_lo, *const b_hi = st + fb + f_hi;
-        const uint8_t *const s_a = st + fsa, *const s_b = st + fsb;
-        v8i a[4], b[2];
-        float sa[4];
-        v4f sb[3], p[kLag + 1];
-        auto row_block = [&](int j) {
-          b[j % 2] = frag_at(b_lo, b_hi, j * 2048);
-          sb[j % 3] = *reinterpret_cast<const v4f*>(s_b + j * 64);
-        };
-        row_block(0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = frag_at(a_lo, a_hi, i * 2048);
-          sa[i] = *reinterpret_cast<const float*>(s_a + i * 64);
-        }
-        // Block k = 4 j + i is folded kLag blocks later, when the matrix core has
-        // written it (held in this order: the compiler would fold it at once, and wait).
-#pragma unroll
-        for (int k = 0; k < 4 * NJ + kLag; ++k) {
-          const int i = k % 4, j = k / 4;
-          if (k < 4 * NJ) {
-            if (i == 0 && j < NJ - 1) row_block(j + 1);
-            v4f& o = p[k % (kLag + 1)];
-            o = v4f{0.f, 0.f, 0.f, 0.f};
-            if constexpr (PRECISE) {
-#pragma unroll
-              for (int h = 0; h < 4; ++h)
-                o = mfma_wide16(widen_quarter(b[j % 2], h), widen_quarter(a[i], h), o);
-            } else {
-              o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j % 2], a[i], o, 0, 0, 0, 0, 0, 0);
-            }
+            for (int h = 0; h < 4; ++h)
+              o = mfma_wide16(widen_quarter(b[j % 2], h), widen_quarter(a[i], h), o);
+          } else {
+            o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j % 2], a[i], o, 0, 0, 0, 0, 0, 0);
           }
-          __builtin_amdgcn_sched_barrier(0);
-          if (k >= kLag) {
-            const int d = k - kLag;
-            promote_rows(acc[d % 4][d / 4], p[d % (kLag + 1)], sa[d % 4], sb[d / 4 % 3]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
         }
+        if (k == kBar) {
+          wait_loads<kStores>(__builtin_amdgcn_readfirstlane(stored));
+          stored = 0;
+          lds_barrier();
+          issue(cur);
+        }
+        if (k == kLast) row_block(st_next, 0, b[0], sb_next);
+        if (k >= kLast && k < 4 * NJ) row_a(st_next, i);
+        __builtin_amdgcn_sched_barrier(0);
+        if (k >= kLag) {
+          const int d = k - kLag;
+          v4f& to = acc[d % 4][d / 4];
+          if constexpr (FIRST) to = v4f{0.f, 0.f, 0.f, 0.f};
+          promote_rows(to, p[d % (kLag + 1)], sa[d % 4], sb[d / 4 % 3]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      lds_barrier();  // the stage is free
+      sb[0] = sb_next;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sa[i] = sa_next[i];
       cur ^= 1;
+    };
+    if (groups > 0) {
+      group(std::true_type{});
+      for (int g = 1; g < groups; ++g) group(std::false_type{});
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
 
-    // Block (i, j): the lane holds n = 16 i + r16, k = 16 j + 4 q .. +3.
-    stored = live;
+    // Block (i, j): the lane holds n = 16 i + r16 and k = 32 (j/2) + 8 q + 4 (j%2) .. +3.
+    stored = live ? 1 : 0;
     if (!live) continue;
-    uint8_t* const c0 = static_cast<uint8_t*>(C) +
-                        (((int64_t)e * N + n0 + (lane >> 3)) * K + k0) * OB + 16 * (lane & 7);
+    const int64_t at = ((int64_t)e * N + n0) * K + k0;
+    const __amdgpu_buffer_rsrc_t rc = make_rsrc(static_cast<uint8_t*>(C) + at * OB,
+                                                (63 * (int64_t)K + NJ * 16) * OB);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j0 = 0; j0 < NJ; j0 += JS) {
-        v4u lo, hi;
+      for (int j = 0; j < NJ; j += OUT_BF16 ? 4 : 2) {
+        v4u x, y;
         if constexpr (OUT_BF16) {
-          v2u p[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            p[j] = v2u{pack_bf16x2(acc[i][j0 + j][0], acc[i][j0 + j][1]),
-                       pack_bf16x2(acc[i][j0 + j][2], acc[i][j0 + j][3])};
-          through_lds(out_w, out_r, p, lo, hi);
+          auto eight = [&](const v4f& l, const v4f& h) {
+            return v4u{pack_bf16x2(l[0], l[1]), pack_bf16x2(l[2], l[3]), pack_bf16x2(h[0], h[1]),
+                       pack_bf16x2(h[2], h[3])};
+          };
+          x = eight(acc[i][j], acc[i][j + 1]);
+          y = eight(acc[i][j + 2], acc[i][j + 3]);
         } else {
-          through_lds(out_w, out_r, acc[i][j0], acc[i][j0 + 1], lo, hi);
+          x = __builtin_bit_cast(v4u, acc[i][j]);
+          y = __builtin_bit_cast(v4u, acc[i][j + 1]);
         }
-        uint8_t* const to = c0 + ((int64_t)(16 * i) * K + 16 * j0) * OB;
-        __builtin_nontemporal_store(lo, reinterpret_cast<v4u*>(to));
-        __builtin_nontemporal_store(hi, reinterpret_cast<v4u*>(to + 8 * (int64_t)K * OB));
+        pair_rows(x, y, odd);
+        const int to = (16 * i * K + 16 * j) * OB;
+        __builtin_amdgcn_raw_buffer_store_b128(x, rc, out_to, to, kNonTemporal);
+        __builtin_amdgcn_raw_buffer_store_b128(y, rc, out_to, to + K * OB, kNonTemporal);
       }
   }
+  wait_vmcnt<0>();  // no load of the stream is under way when the wave ends
 }
 
 template <class Cfg, bool PRECISE, bool OUT_BF16>
@@ -358,9 +404,7 @@ static hipError_t launch(const uint8_t* a_q, const float* a_s, const uint8_t* b_
                          int64_t T, const int32_t* off, int G, int64_t N, int64_t K, void* c,
                          int out_bf16, int precise, int cus, hipStream_t stream) {
   const int64_t tiles_k = (K + Cfg::TK - 1) / Cfg::TK, tiles = (N + Cfg::TN - 1) / Cfg::TN * tiles_k;
-  // (tile numbers, rows and columns are ints)
-  if (tiles > 0x7FFFFFFF / (G + 1) - 1024 || N > 0x7FFFFF00 || K > 0x7FFFFF00)
-    return hipErrorInvalidValue;
+  if (tiles > 0x7FFFFFFF / (G + 1) - 1024) return hipErrorInvalidValue;  // (tile numbers are ints)
   int64_t grid = (int64_t)cus * Cfg::PER_CU;
   if (grid > tiles * G) grid = tiles * G;
   grid = (grid + kXcds - 1) / kXcds * kXcds;

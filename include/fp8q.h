@@ -561,8 +561,8 @@ fp8q_status fp8q_grouped_gated_backward(const void* dh, const void* gate_up, int
  *         asks for (fewer: invalid offsets).
  *   c   : [G][N][K] float32 or bfloat16 (per `out`) (output); zeros for an expert
  *         without rows.
- *   N % 128 == 0, K % 128 == 0.  FP8Q_ERR_UNSUPPORTED: G > 1024, T > 2^24 (32-bit
- *   load offsets).
+ *   N % 128 == 0, K % 128 == 0.  FP8Q_ERR_UNSUPPORTED: G > 1024, T > 2^24, N or K
+ *   > 2^22 (32-bit offsets).
  * Accuracy: the ACCURACY clause of fp8q_gemm over each expert's groups, and for the
  * precise call that of fp8q_gemm_precise.
  */
