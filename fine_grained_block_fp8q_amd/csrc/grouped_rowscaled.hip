@@ -8,23 +8,33 @@
 // is formed by the FP8 matrix core from zero and folded into FP32 sums with the
 // product of its two scales, as in the dense row-scaled GEMM.
 //
-// An expert has few tokens (128 .. 1024) for a large C, so that the call is bound
-// by writing C, and a tile of C has few groups to sum: what costs time is the
-// latency at a tile's start and end.  A persistent workgroup of 4 waves therefore
-// walks tiles of 128 x 128 (64 x 64 a wave) as one stream of groups: the next
-// group's loads, the next tile's first one among them, go out before a group is
-// computed, and a tile's stores drain while the next is summed.  Two workgroups a
-// CU, two stages of one group each in LDS (direct loads; rows of 128 bytes with
-// exchanged 16-byte columns, swz, so that fragment reads are free of conflicts).
-// The product is formed transposed (matrix-core rows are B's rows), so that a
-// lane's four results are consecutive in k; the lanes of two rows exchange theirs in
-// registers, so that 8 lanes store a row's 128 consecutive bytes at once (4 lanes and
-// 64 bytes: 622 us where this takes 4xx; through LDS: 517).
+// An expert has few tokens (128 .. 1024) for a large C: a tile of C has few groups
+// to sum, and what costs time beside the products is the latency at a tile's start
+// and the writing of C.  A persistent workgroup therefore walks tiles as one stream
+// of groups: while a group is multiplied the next one's loads are on their way, a
+// tile's last group's and the next tile's first one among them, and the next
+// group's fragments come into registers before the current one's last products.
+// Two stages of one group each in LDS (direct loads; rows of 128 bytes with
+// exchanged 16-byte columns, so that fragment reads are free of conflicts).  The
+// product is formed transposed (matrix-core rows are B's rows, in an order that
+// gives a lane 8 consecutive k of two blocks), and the lanes of two rows exchange
+// pieces, so that 8 lanes store a row's 128 bytes at once (4 lanes and 64 bytes:
+// 622 us where whole lines take 522).
+//
+// Tiles of 256 x 256 (8 waves of 64 x 128, one workgroup a CU) where they fill the
+// chip 5 times over, else 128 x 128 (4 waves of 64 x 64, two workgroups a CU), us:
+//   tiles of 256 x 256         512    576    1024   1280   2048   14336
+//   256 x 256                  21.4   42.7   37.0   58.9   54.1   470
+//   128 x 128                  17.9   28.7   35.0   60.7   55.1   744
 //
 // Each XCD takes a run of the tiles (all of an expert's follow each other: its
-// operands stay in that XCD's L2), cut so that the runs' groups, plus
-// kTileCost for every tile's stores, are equal; its workgroups take the run's
-// tiles in turn.
+// operands stay in that XCD's L2), cut so that the runs' groups, plus kTileCost for
+// every tile, are equal; its workgroups take the run's tiles in turn.
+//
+// 32 experts, 8192 tokens, 4096 x 7168 in BF16 (1.88 GB of C, 2.5 groups a tile): 470
+// .. 500 us, 4.2 TB/s; loads alone take 222, loads and products with nothing stored
+// 395, stores of this pattern alone 350.  16 experts of 1000 tokens, 7168 x 2048: 311
+// us, 1.51 PFLOP/s.
 
 #include "experts.hpp"
 #include "fp8q.h"
@@ -54,8 +64,8 @@ using WgSmall = WgCfg<128, 128, 2, 2, 2>;
 constexpr int kWgExperts = 1024;
 constexpr int kNonTemporal = 2;         // cache policy bit of a buffer store
 constexpr int kLag = 2;                 // blocks between a product and its folding
-constexpr int64_t kLargeTiles = 2;      // of 256 x 256 a CU, from which they are taken
-constexpr int kTileCost = 2;            // a tile's stores, in groups
+constexpr int64_t kLargeTiles = 5;      // of 256 x 256 a CU, from which they are taken
+constexpr int kTileCost = 1;            // of a tile beside its groups, in groups
 
 template <class Cfg>
 struct WgShared {
@@ -70,7 +80,7 @@ static_assert(WgLarge::PER_CU * sizeof(WgShared<WgLarge>) <= 160 * 1024 &&
 // one's, x becomes the even row's x and y, y the odd row's.
 __device__ __forceinline__ void pair_rows(v4u& x, v4u& y, bool odd) {
   auto other = [](uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppQuadXor1, 0xF, 0xF, false);
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kDppQuadXor1, 0xF, 0xF, false);
   };
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
@@ -132,19 +142,21 @@ __device__ __forceinline__ bool expert_prefix(const int32_t* off, int G, int64_t
   return true;
 }
 
-// First tile of share x of `shares` equal ones, by cost: tiles * (groups + kTileCost)
-// an expert.
-__device__ __forceinline__ int share_start(const int* group0, int G, int tiles, int x, int shares) {
-  auto cost = [&](int e) { return (int64_t)tiles * (group0[e] + (int64_t)kTileCost * e); };
-  const int64_t want = cost(G) * x / shares;
+// First tile of run x of the kXcds equal ones, by cost: tiles * (groups + kTileCost) an
+// expert.
+__device__ __forceinline__ int run_start(const int* group0, int G, int tiles, int x) {
+  auto cost = [&](int e) { return (uint64_t)tiles * (uint64_t)(group0[e] + kTileCost * e); };
+  const uint64_t want = cost(G) * (uint64_t)x / kXcds;
   int lo = 0, hi = G;  // cost(lo) <= want < cost(hi), or want is the end
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (cost(mid) <= want) lo = mid; else hi = mid;
   }
-  const int each = group0[lo + 1] - group0[lo] + kTileCost;
-  const int64_t in = (want - cost(lo)) / each;
-  return lo * tiles + (int)(in < tiles ? in : tiles);
+  const uint32_t each = (uint32_t)(group0[lo + 1] - group0[lo] + kTileCost);
+  const uint64_t rest = want - cost(lo);
+  // (a division of 64 bits takes long: only where one is needed)
+  const uint64_t in = rest >> 32 ? rest / each : (uint32_t)rest / each;
+  return lo * tiles + (int)(in < (uint64_t)tiles ? in : (uint64_t)tiles);
 }
 
 // A fragment's two 16-byte pieces.
@@ -167,9 +179,9 @@ __device__ __forceinline__ void grouped_rowscaled(
   }
   __syncthreads();
   const int x = blockIdx.x % kXcds, step = gridDim.x / kXcds;
-  const int first = __builtin_amdgcn_readfirstlane(share_start(sh.group0, G, tiles, x, kXcds)) +
+  const int first = __builtin_amdgcn_readfirstlane(run_start(sh.group0, G, tiles, x)) +
                     (int)(blockIdx.x / kXcds);
-  const int end = __builtin_amdgcn_readfirstlane(share_start(sh.group0, G, tiles, x + 1, kXcds));
+  const int end = __builtin_amdgcn_readfirstlane(run_start(sh.group0, G, tiles, x + 1));
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -253,6 +265,7 @@ __device__ __forceinline__ void grouped_rowscaled(
 
   constexpr int OB = OUT_BF16 ? 2 : 4;
   constexpr int kStores = Cfg::STORES * OB / 2;
+  constexpr int kWide = OUT_BF16 ? 4 : 2;  // blocks of 128 bytes
   const bool odd = r16 & 1;
   const uint32_t out_to =
       (uint32_t)((r16 - odd) * K * OB + (OUT_BF16 ? odd * 64 + 16 * q : odd * 16 + 32 * q));
@@ -276,8 +289,12 @@ __device__ __forceinline__ void grouped_rowscaled(
   advance();
   issue(0);
   advance();
-  issue(1);
-  wait_vmcnt<Cfg::LOADS>();
+  if (lt < end) {
+    issue(1);
+    wait_vmcnt<Cfg::LOADS>();
+  } else {
+    wait_vmcnt<0>();
+  }
   lds_barrier();
   row_block(sh.stage[0], 0, b[0], sb[0]);
 #pragma unroll
@@ -356,13 +373,11 @@ __device__ __forceinline__ void grouped_rowscaled(
     // Block (i, j): the lane holds n = 16 i + r16 and k = 32 (j/2) + 8 q + 4 (j%2) .. +3.
     stored = live ? 1 : 0;
     if (!live) continue;
-    const int64_t at = ((int64_t)e * N + n0) * K + k0;
-    const __amdgpu_buffer_rsrc_t rc = make_rsrc(static_cast<uint8_t*>(C) + at * OB,
-                                                (63 * (int64_t)K + NJ * 16) * OB);
+    uint8_t* const c0 = static_cast<uint8_t*>(C) + (((int64_t)e * N + n0) * K + k0) * OB;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; j += OUT_BF16 ? 4 : 2) {
+      for (int j = 0; j < NJ; j += kWide) {
         v4u x, y;
         if constexpr (OUT_BF16) {
           auto eight = [&](const v4f& l, const v4f& h) {
@@ -376,12 +391,18 @@ __device__ __forceinline__ void grouped_rowscaled(
           y = __builtin_bit_cast(v4u, acc[i][j + 1]);
         }
         pair_rows(x, y, odd);
-        const int to = (16 * i * K + 16 * j) * OB;
-        __builtin_amdgcn_raw_buffer_store_b128(x, rc, out_to, to, kNonTemporal);
-        __builtin_amdgcn_raw_buffer_store_b128(y, rc, out_to, to + K * OB, kNonTemporal);
+        // (The place is in the resource, not a scalar offset: for a store with one the
+        // compiler puts no wait before the next instruction, which may then write the
+        // data's first register before the last lanes have sent it.)
+        uint8_t* const to = c0 + ((int64_t)16 * i * K + 16 * j) * OB;
+        const int64_t rows = ((int64_t)14 * K + 16 * kWide) * OB;
+        __builtin_amdgcn_raw_buffer_store_b128(x, make_rsrc(to, rows), out_to, 0, kNonTemporal);
+        __builtin_amdgcn_raw_buffer_store_b128(y, make_rsrc(to + (int64_t)K * OB, rows), out_to, 0,
+                                               kNonTemporal);
       }
   }
-  wait_vmcnt<0>();  // no load of the stream is under way when the wave ends
+  // No load into LDS is under way when the wave ends (the last tile's stores may be).
+  wait_loads<kStores>(__builtin_amdgcn_readfirstlane(stored));
 }
 
 template <class Cfg, bool PRECISE, bool OUT_BF16>
@@ -399,19 +420,17 @@ hipError_t wgrad_offsets_error_take(hipStream_t stream, int* flag) {
 }
 #endif
 
-template <class Cfg>
+template <class Cfg, bool PRECISE>
 static hipError_t launch(const uint8_t* a_q, const float* a_s, const uint8_t* b_q, const float* b_s,
                          int64_t T, const int32_t* off, int G, int64_t N, int64_t K, void* c,
-                         int out_bf16, int precise, int cus, hipStream_t stream) {
+                         int out_bf16, int cus, hipStream_t stream) {
   const int64_t tiles_k = (K + Cfg::TK - 1) / Cfg::TK, tiles = (N + Cfg::TN - 1) / Cfg::TN * tiles_k;
   if (tiles > 0x7FFFFFFF / (G + 1) - 1024) return hipErrorInvalidValue;  // (tile numbers are ints)
   int64_t grid = (int64_t)cus * Cfg::PER_CU;
   if (grid > tiles * G) grid = tiles * G;
   grid = (grid + kXcds - 1) / kXcds * kXcds;
-  auto kern = precise ? (out_bf16 ? grouped_rowscaled_kernel<Cfg, true, true>
-                                  : grouped_rowscaled_kernel<Cfg, true, false>)
-                      : (out_bf16 ? grouped_rowscaled_kernel<Cfg, false, true>
-                                  : grouped_rowscaled_kernel<Cfg, false, false>);
+  auto kern = out_bf16 ? grouped_rowscaled_kernel<Cfg, PRECISE, true>
+                       : grouped_rowscaled_kernel<Cfg, PRECISE, false>;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::THREADS), 0, stream, a_q, a_s, b_q, b_s,
                      off, G, T, (int)N, (int)K, c, (int)tiles_k, (int)tiles);
   return hipGetLastError();
@@ -427,9 +446,10 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t* a_q, const float* a_s, c
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
     return hipGetLastError();
   const int64_t large = (N + 255) / 256 * ((K + 255) / 256) * G;
-  if (large >= kLargeTiles * cus)
-    return launch<WgLarge>(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, precise, cus, stream);
-  return launch<WgSmall>(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, precise, cus, stream);
+  if (large >= kLargeTiles * cus && !precise)  // (widened to FP16, its fragments would spill)
+    return launch<WgLarge, false>(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, cus, stream);
+  return (precise ? launch<WgSmall, true> : launch<WgSmall, false>)(
+      a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, cus, stream);
 }
 
 }  // namespace fp8q

@@ -138,6 +138,31 @@ def test_grouped_gemm_rowscaled(name, N, K, out, precise):
     _check(c, ops, off, out, precise, f"{name} {N}x{K}")
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("name,N,K", [("65 experts", 640, 1664), ("65 experts", 640, 1152),
+                                      ("1024 experts", 128, 384), ("ragged", 4224, 7296),
+                                      ("rows behind", 1024, 128), ("first and last empty", 128, 1024)])
+def test_every_tile_size_equals_the_dense_call(name, N, K, out):
+    """Large and small tiles, ending inside the outputs in both directions: each
+    expert's gradient is the dense call's on its columns, bit for bit (the same sums
+    in the same order)."""
+    off, M, off_d = _split(name)
+    qa, sa, qb, sb = _operands(off, M, off_d, N, K, 7)
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    c = fq().grouped_gemm_rowscaled(qa, sa, qb, sb, off_d, out_dtype=dt)
+    at = 0
+    for e in range(len(off) - 1):
+        w = -(-int(off[e + 1] - off[e]) // 128) * 128
+        if w == 0:
+            assert not c[e].any()
+            continue
+        cols, g = slice(at, at + w), slice(at // 128, (at + w) // 128)
+        at += w
+        want = fq().gemm_rowscaled(qa[:, cols].contiguous(), sa[g], qb[:, cols].contiguous(), sb[g],
+                                   out_dtype=dt)
+        assert torch.equal(c[e], want), f"expert {e}"
+
+
 @pytest.mark.parametrize("tokens", [1000, 2500])
 def test_grouped_gemm_rowscaled_long(tokens):
     """Experts of many groups, and one expert's gradient against the dense call's."""
