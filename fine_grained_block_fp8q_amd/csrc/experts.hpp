@@ -35,14 +35,28 @@ __device__ __forceinline__ ExpertSpan expert_span(const int32_t* off, int G, int
   const int lane = threadIdx.x & 63;
   const int PL = (G + 63) >> 6;  // uniform
   const int e0 = lane * PL;
+  constexpr int UP = 4;  // experts whose offsets are loaded together
+  // f(expert, its first row, its rows) of the lane's experts, until it says so
+  auto each = [&](auto f) {
+    for (int i = 0; i < PL; i += UP) {
+      int o[UP + 1];
+#pragma unroll
+      for (int u = 0; u <= UP; ++u) {
+        const int at = e0 + i + u;
+        o[u] = off[at < G ? at : G];
+      }
+#pragma unroll
+      for (int u = 0; u < UP; ++u)
+        if (i + u < PL && e0 + i + u < G && f(e0 + i + u, o[u], o[u + 1] - o[u])) return;
+    }
+  };
   int sum = 0;
   bool bad = lane == 0 && (off[0] != 0 || (int64_t)off[G] > M);
-  for (int i = 0; i < PL; ++i)
-    if (e0 + i < G) {
-      const int lo = off[e0 + i], hi = off[e0 + i + 1];
-      bad = bad || hi < lo;
-      sum += groups_of(hi - lo);
-    }
+  each([&](int, int lo, int n) {
+    bad = bad || n < 0 || lo < 0;
+    sum += groups_of(n);
+    return false;
+  });
   ExpertSpan r = {-1, 0, 0, 0};
   if (__ballot(bad) != 0) return r;
   int inc = sum;
@@ -55,17 +69,18 @@ __device__ __forceinline__ ExpertSpan expert_span(const int32_t* off, int G, int
   int at = inc - sum, first = 0, rows = 0, group0 = 0;
   const bool mine = BY_GROUP ? want >= at && want < inc : want >= e0 && want < e0 + PL;
   if (mine)
-    for (int i = 0; i < PL && e0 + i < G; ++i) {
-      const int lo = off[e0 + i], n = off[e0 + i + 1] - lo, g = groups_of(n);
-      if (BY_GROUP ? want < at + g : want == e0 + i) {
+    each([&](int e, int lo, int n) {
+      const int g = groups_of(n);
+      if (BY_GROUP ? want < at + g : want == e) {
         const int skip = BY_GROUP ? (want - at) * 128 : 0;
         first = lo + skip;
         rows = BY_GROUP && n - skip > 128 ? 128 : n - skip;
         group0 = at;
-        break;
+        return true;
       }
       at += g;
-    }
+      return false;
+    });
   const uint64_t who = __ballot(mine);
   r.status = 0;
   if (who == 0) return r;
