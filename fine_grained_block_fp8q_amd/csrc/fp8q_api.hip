@@ -568,8 +568,8 @@ fp8q_status fp8q_layer_norm_backward(const void* dy, fp8q_out_dtype dy_type, con
                                      void* dx, float* dweight, float* dbias, void* workspace,
                                      hipStream_t stream) {
   if (!dweight) return FP8Q_ERR_NULL;
-  if (M != 0 && (!dy || !x || !weight || !mean || !rstd || !dx || !workspace))
-    return FP8Q_ERR_NULL;
+  if (M != 0 && (!dy || !x || !weight || !mean || !rstd || !dx)) return FP8Q_ERR_NULL;
+  if (!workspace && fp8q_layer_norm_backward_workspace(M, N) != 0) return FP8Q_ERR_NULL;
   if (M < 0 || N < 1) return FP8Q_ERR_SHAPE;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(workspace, 16) ||
       !aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) ||

@@ -33,37 +33,41 @@ struct Row8 {
   float v[8];
 };
 
-// Elements 8c .. 8c+7 of a row of n; those past the row are 0.
+// Elements 8c .. 8c+7 of a row of n as they are in memory; those past the row are 0.
+// WHOLE: n is a multiple of 8, no piece ends early (the code for one that does takes
+// registers, which in the backward pass are the rows under way).
 template <bool BF16>
-__device__ __forceinline__ Row8 load8(const void* row, int c, int n) {
-  Row8 r;
+struct Raw8 {
+  v4u w[BF16 ? 1 : 2];
+};
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ Raw8<BF16> load_raw(const void* row, int c, int n) {
+  Raw8<BF16> r;
   const int i = 8 * c;
   if (i + 8 <= n) {
-    if constexpr (BF16) {
-      const v4u w = *reinterpret_cast<const v4u_any*>(static_cast<const uint16_t*>(row) + i);
+    const char* at = static_cast<const char*>(row) + (int64_t)i * (BF16 ? 2 : 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r.v[2 * j] = bf16_lo(w[j]);
-        r.v[2 * j + 1] = bf16_hi(w[j]);
-      }
-    } else {
-      const v4f a = *reinterpret_cast<const v4f_any*>(static_cast<const float*>(row) + i);
-      const v4f b = *reinterpret_cast<const v4f_any*>(static_cast<const float*>(row) + i + 4);
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = *reinterpret_cast<const v4u_any*>(at + 16 * h);
+  } else if (WHOLE) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r.v[j] = a[j];
-        r.v[4 + j] = b[j];
-      }
-    }
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) r.w[h] = v4u{0, 0, 0, 0};
   } else {
+    uint32_t e[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      r.v[j] = 0.f;
-      if (i + j < n) {
-        if constexpr (BF16)
-          r.v[j] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(row)[i + j] << 16);
-        else
-          r.v[j] = static_cast<const float*>(row)[i + j];
+      e[j] = 0;
+      if (i + j < n)
+        e[j] = BF16 ? (uint32_t)static_cast<const uint16_t*>(row)[i + j]
+                    : static_cast<const uint32_t*>(row)[i + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF16) {
+        r.w[0][j] = e[2 * j] | (e[2 * j + 1] << 16);
+      } else {
+        r.w[0][j] = e[j];
+        r.w[1][j] = e[4 + j];
       }
     }
   }
@@ -71,9 +75,30 @@ __device__ __forceinline__ Row8 load8(const void* row, int c, int n) {
 }
 
 template <bool BF16>
+__device__ __forceinline__ Row8 widened(const Raw8<BF16>& r) {
+  Row8 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (BF16) {
+      o.v[2 * j] = bf16_lo(r.w[0][j]);
+      o.v[2 * j + 1] = bf16_hi(r.w[0][j]);
+    } else {
+      o.v[j] = __uint_as_float(r.w[0][j]);
+      o.v[4 + j] = __uint_as_float(r.w[1][j]);
+    }
+  }
+  return o;
+}
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ Row8 load8(const void* row, int c, int n) {
+  return widened<BF16>(load_raw<BF16, WHOLE>(row, c, n));
+}
+
+template <bool BF16, bool WHOLE>
 __device__ __forceinline__ void store8(void* row, int c, int n, const Row8& r) {
   const int i = 8 * c;
-  if (i + 8 <= n) {
+  if (WHOLE || i + 8 <= n) {  // (the caller's pieces begin within the row)
     if constexpr (BF16) {
       v4u w;
 #pragma unroll
@@ -147,6 +172,8 @@ struct NormArgs {
   float* rstd;
 };
 
+constexpr int kCus = 256;
+
 template <int LPR>
 constexpr int kRowThreads = LPR < 256 ? 256 : LPR;
 
@@ -164,7 +191,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t row, int 
   if ((threadIdx.x & 15) == 0) a.s[(int64_t)(c >> 4) * a.M + row] = r.s;
 }
 
-template <bool X_BF16, int LPR, int NV>
+template <bool X_BF16, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_kernel(const NormArgs a) {
   __shared__ float red[2][1][16];
   constexpr int RPW = kRowThreads<LPR> / LPR;
@@ -177,7 +204,7 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_kernel(const Norm
   float sum[1] = {0.f};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    v[j] = load8<X_BF16>(x, l + LPR * j, N);
+    v[j] = load8<X_BF16, WHOLE>(x, l + LPR * j, N);
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[0] += v[j].v[k];
   }
@@ -202,10 +229,10 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_kernel(const Norm
   for (int j = 0; j < NV; ++j) {
     const int c = l + LPR * j;
     if (8 * c >= N) continue;
-    const Row8 w = load8<false>(a.weight, c, N);
+    const Row8 w = load8<false, WHOLE>(a.weight, c, N);
     Row8 y;
     if (a.bias) {
-      const Row8 b = load8<false>(a.bias, c, N);
+      const Row8 b = load8<false, WHOLE>(a.bias, c, N);
 #pragma unroll
       for (int k = 0; k < 8; ++k) y.v[k] = __builtin_fmaf(v[j].v[k] * rstd, w.v[k], b.v[k]);
     } else {
@@ -220,16 +247,14 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_kernel(const Norm
     }
     if (a.y) {
       if (a.y_bf16)
-        store8<true>(row_at(a.y, row, N, true), c, N, y);
+        store8<true, WHOLE>(row_at(a.y, row, N, true), c, N, y);
       else
-        store8<false>(row_at(a.y, row, N, false), c, N, y);
+        store8<false, WHOLE>(row_at(a.y, row, N, false), c, N, y);
     }
   }
 }
 
 // ------------------------------------------------------------------ backward
-constexpr int kNormBlocks = 256;  // workgroups that walk the rows: one a CU
-
 struct NormBwArgs {
   const void* dy;
   const void* x;
@@ -239,10 +264,12 @@ struct NormBwArgs {
   int64_t M;
   int N;
   void* dx;
-  float* part;  // [workgroups][2][N]
+  float* dw;        // of workgroup b: dw + b * stride, db + b * stride
+  float* db;        // (one workgroup: the results themselves; db may then be NULL)
+  int64_t stride;
 };
 
-template <bool X_BF16, bool DY_BF16, int LPR, int NV>
+template <bool X_BF16, bool DY_BF16, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(const NormBwArgs a) {
   __shared__ float red[2][2][16];
   constexpr int RPW = kRowThreads<LPR> / LPR;
@@ -254,23 +281,39 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(c
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[j][k] = db[j][k] = 0.f;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < a.M; row += (int64_t)gridDim.x * RPW) {
-    const void* x = row_at(a.x, row, N, X_BF16);
-    const void* dy = row_at(a.dy, row, N, DY_BF16);
-    const float mean = a.mean[row], rstd = a.rstd[row];
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  int64_t row = (int64_t)blockIdx.x * RPW + sub;
+  // The next two rows' values are on their way while one is worked on (of the widest
+  // rows there are no registers for them).
+  constexpr bool kAhead = LPR * NV < 2048;
+  struct Values {
+    Raw8<X_BF16> x[NV];
+    Raw8<DY_BF16> dy[NV];
+    float mean, rstd;
+  };
+  auto load = [&](Values& v, int64_t r) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      v.x[j] = load_raw<X_BF16, WHOLE>(row_at(a.x, r, N, X_BF16), l + LPR * j, N);
+      v.dy[j] = load_raw<DY_BF16, WHOLE>(row_at(a.dy, r, N, DY_BF16), l + LPR * j, N);
+    }
+    v.mean = a.mean[r];
+    v.rstd = a.rstd[r];
+  };
+  // Row `row`, whose values are in v, which then takes those of the row after the next.
+  auto one = [&](Values& v, float (*red)[16]) {
+    const float mean = v.mean, rstd = v.rstd;
     Row8 z[NV], g[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      z[j] = widened<X_BF16>(v.x[j]);
+      g[j] = widened<DY_BF16>(v.dy[j]);
+    }
+    if (kAhead && row + 2 * step < a.M) load(v, row + 2 * step);
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = l + LPR * j;
-      z[j] = load8<X_BF16>(x, c, N);
-      g[j] = load8<DY_BF16>(dy, c, N);
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = l + LPR * j;
-      const Row8 w = load8<false>(a.weight, c, N);
+      const Row8 w = load8<false, WHOLE>(a.weight, l + LPR * j, N);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float zz = (z[j].v[k] - mean) * rstd;  // (past the row: times a 0 of dy)
@@ -282,8 +325,7 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(c
         sum[1] = __builtin_fmaf(g[j].v[k], zz, sum[1]);
       }
     }
-    row_sum<LPR, 2>(sum, red[turn]);
-    turn ^= 1;
+    row_sum<LPR, 2>(sum, red);
     const float c2 = sum[0] * inv_n, c1 = sum[1] * inv_n;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -291,8 +333,21 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(c
       Row8 d;
 #pragma unroll
       for (int k = 0; k < 8; ++k) d.v[k] = rstd * (g[j].v[k] - c2 - z[j].v[k] * c1);
-      if (8 * c < N) store8<X_BF16>(row_at(a.dx, row, N, X_BF16), c, N, d);
+      if (8 * c < N) store8<X_BF16, WHOLE>(row_at(a.dx, row, N, X_BF16), c, N, d);
     }
+    row += step;
+  };
+  Values v0, v1;
+  if (kAhead) {
+    if (row < a.M) load(v0, row);
+    if (row + step < a.M) load(v1, row + step);
+  }
+  while (row < a.M) {
+    if (!kAhead) load(v0, row);
+    one(v0, red[0]);
+    if (row >= a.M) break;
+    if (!kAhead) load(v1, row);
+    one(v1, red[1]);
   }
   if constexpr (RPW > 1) {
     // the waves' sums of the same columns, one wave after the other
@@ -315,7 +370,6 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(c
           db[j][k] += part[1][s][j][k][l];
         }
   }
-  float* out = a.part + (int64_t)blockIdx.x * 2 * N;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = l + LPR * j;
@@ -326,91 +380,130 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(c
       b.v[k] = db[j][k];
     }
     if (8 * c < N) {
-      store8<false>(out, c, N, w);
-      store8<false>(out + N, c, N, b);
+      store8<false, WHOLE>(a.dw + blockIdx.x * a.stride, c, N, w);
+      if (a.db) store8<false, WHOLE>(a.db + blockIdx.x * a.stride, c, N, b);
     }
   }
 }
 
-// Column sums of part[rows][2N]: 64 columns x 4 slices of the rows a workgroup.
-__global__ __launch_bounds__(256) void layer_norm_reduce_kernel(const float* __restrict__ part,
-                                                                int rows, int N,
-                                                                float* __restrict__ dweight,
-                                                                float* __restrict__ dbias) {
-  __shared__ float red[4][64];
-  const int l = threadIdx.x & 63, slice = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + l;
-  const int64_t ld = 2 * (int64_t)N;
+// Column sums of part[rows][2N]: 32 columns x 32 slices of the rows a workgroup.
+__global__ __launch_bounds__(1024) void layer_norm_reduce_kernel(const float* __restrict__ part,
+                                                                 int rows, int N,
+                                                                 float* __restrict__ dweight,
+                                                                 float* __restrict__ dbias) {
+  __shared__ float red[32][33];
+  const int l = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t ld = 2 * (int64_t)N, col = (int64_t)blockIdx.x * 32 + l;
   float s = 0.f;
   if (col < ld) {
-    const int r0 = (int)((int64_t)rows * slice / 4), r1 = (int)((int64_t)rows * (slice + 1) / 4);
-#pragma unroll 8
-    for (int r = r0; r < r1; ++r) s += part[r * ld + col];
+    // slice, slice + 32, ...: the rows that are loaded together follow each other
+#pragma unroll 4
+    for (int r = slice; r < rows; r += 32) s += part[r * ld + col];
   }
   red[slice][l] = s;
   __syncthreads();
-  if (slice != 0 || col >= ld) return;
-  s = red[0][l] + red[1][l] + red[2][l] + red[3][l];
-  if (col < N)
-    dweight[col] = s;
+  // lane i of a wave's half adds up column `slice`
+  s = red[l][slice];
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor(s, d);
+  const int64_t out = (int64_t)blockIdx.x * 32 + slice;
+  if (l != 0 || out >= ld) return;
+  if (out < N)
+    dweight[out] = s;
   else if (dbias)
-    dbias[col - N] = s;
+    dbias[out - N] = s;
 }
 
 // ------------------------------------------------------------------ launches
-// Lanes of a row and pieces of a lane: the fewest pieces that fit the row.
-template <class F>
+// Lanes of a row and pieces of a lane that fit the row, for both passes.  The wide
+// rows of the forward pass take two pieces a lane (4096 rows of 7168: 42 us, one piece
+// 48); those of the backward pass one, which leaves registers for the rows under way.
+template <int LPR, int NV>
+struct Width {
+  static constexpr int kLpr = LPR, kNv = NV;
+};
+
+template <bool BACKWARD, class F>
 static hipError_t by_width(int64_t N, F f) {
   const int64_t c = (N + 7) / 8;
-  if (c <= 64) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (c <= 128) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  if (c <= 256) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  if (c <= 512) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (c <= 1024) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  auto g = [&](auto w) {
+    return N % 8 == 0 ? f(w, std::true_type{}) : f(w, std::false_type{});
+  };
+  if (c <= 64) return g(Width<64, 1>{});
+  if (c <= 128) return g(Width<64, 2>{});
+  if (c <= 256) return g(Width<256, 1>{});
+  if constexpr (BACKWARD) {
+    if (c <= 512) return g(Width<512, 1>{});
+    if (c <= 1024) return g(Width<1024, 1>{});
+  } else {
+    if (c <= 512) return g(Width<256, 2>{});
+    if (c <= 1024) return g(Width<512, 2>{});
+  }
+  return g(Width<1024, 2>{});
 }
 
 hipError_t launch_layer_norm(const void* x, int x_bf16, const float* weight, const float* bias,
                              int64_t M, int64_t N, float eps, void* y, int y_bf16, uint8_t* q,
                              float* s, int mode, float* mean, float* rstd, hipStream_t stream) {
   const NormArgs a = {x, weight, bias, M, (int)N, eps, y, y_bf16, q, s, mode, mean, rstd};
-  return by_width(N, [&](auto lpr, auto nv) {
-    constexpr int LPR = decltype(lpr)::value, NV = decltype(nv)::value, T = kRowThreads<LPR>;
+  return by_width<false>(N, [&](auto w, auto whole) {
+    constexpr int LPR = decltype(w)::kLpr, NV = decltype(w)::kNv, T = kRowThreads<LPR>;
+    constexpr bool WHOLE = decltype(whole)::value;
     const int64_t blocks = (M + T / LPR - 1) / (T / LPR);
     if (blocks > max_blocks(T)) return hipErrorInvalidValue;
-    auto kern = x_bf16 ? layer_norm_kernel<true, LPR, NV> : layer_norm_kernel<false, LPR, NV>;
+    auto kern = x_bf16 ? layer_norm_kernel<true, LPR, NV, WHOLE>
+                       : layer_norm_kernel<false, LPR, NV, WHOLE>;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(T), 0, stream, a);
     return hipGetLastError();
   });
 }
 
+// Workgroups of the backward pass.  One for a few rows (it writes the results
+// itself); else enough to fill the chip, but with kRowsEach rows for each lane group
+// at least, so that what the workgroups leave to be added up stays small.
+constexpr int kNormThreads = 1024 * 256, kRowsEach = 8, kRowsAlone = 2;
+
 static int64_t norm_backward_blocks(int64_t M, int64_t N) {
-  const int64_t rpw = N <= 1024 ? 4 : 1;
-  const int64_t all = (M + rpw - 1) / rpw;
-  return all < kNormBlocks ? all : kNormBlocks;
+  int64_t blocks = 0;
+  (void)by_width<true>(N, [&](auto w, auto) {
+    constexpr int LPR = decltype(w)::kLpr, T = kRowThreads<LPR>, RPW = T / LPR;
+    const int64_t rows = (M + RPW - 1) / RPW, most = kNormThreads / T;
+    blocks = (rows + kRowsEach - 1) / kRowsEach;
+    blocks = blocks > most ? most : blocks;
+    const int64_t least = rows < kCus ? rows : kCus;
+    blocks = rows <= kRowsAlone ? 1 : blocks < least ? least : blocks;
+    return hipSuccess;
+  });
+  return M == 0 ? 0 : blocks;
 }
 
 int64_t layer_norm_backward_workspace(int64_t M, int64_t N) {
-  return norm_backward_blocks(M, N) * 2 * N * 4;
+  const int64_t blocks = norm_backward_blocks(M, N);
+  return blocks > 1 ? blocks * 2 * N * 4 : 0;
 }
 
 hipError_t launch_layer_norm_backward(const void* dy, int dy_bf16, const void* x, int x_bf16,
                                       const float* weight, const float* mean, const float* rstd,
                                       int64_t M, int64_t N, void* dx, float* dweight, float* dbias,
                                       float* workspace, hipStream_t stream) {
-  const NormBwArgs a = {dy, x, weight, mean, rstd, M, (int)N, dx, workspace};
   const int blocks = (int)norm_backward_blocks(M, N);
-  const hipError_t e = blocks == 0 ? hipSuccess : by_width(N, [&](auto lpr, auto nv) {
-    constexpr int LPR = decltype(lpr)::value, NV = decltype(nv)::value;
-    auto kern = x_bf16 ? (dy_bf16 ? layer_norm_backward_kernel<true, true, LPR, NV>
-                                  : layer_norm_backward_kernel<true, false, LPR, NV>)
-                       : (dy_bf16 ? layer_norm_backward_kernel<false, true, LPR, NV>
-                                  : layer_norm_backward_kernel<false, false, LPR, NV>);
+  NormBwArgs a = {dy, x, weight, mean, rstd, M, (int)N, dx, workspace, workspace + N, 2 * N};
+  if (blocks == 1) {
+    a.dw = dweight;
+    a.db = dbias;
+  }
+  const hipError_t e = blocks == 0 ? hipSuccess : by_width<true>(N, [&](auto w, auto whole) {
+    constexpr int LPR = decltype(w)::kLpr, NV = decltype(w)::kNv;
+    constexpr bool WHOLE = decltype(whole)::value;
+    auto kern = x_bf16 ? (dy_bf16 ? layer_norm_backward_kernel<true, true, LPR, NV, WHOLE>
+                                  : layer_norm_backward_kernel<true, false, LPR, NV, WHOLE>)
+                       : (dy_bf16 ? layer_norm_backward_kernel<false, true, LPR, NV, WHOLE>
+                                  : layer_norm_backward_kernel<false, false, LPR, NV, WHOLE>);
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kRowThreads<LPR>), 0, stream, a);
     return hipGetLastError();
   });
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(layer_norm_reduce_kernel, dim3((unsigned)((2 * N + 63) / 64)), dim3(256), 0,
+  if (e != hipSuccess || blocks == 1) return e;
+  hipLaunchKernelGGL(layer_norm_reduce_kernel, dim3((unsigned)((2 * N + 31) / 32)), dim3(1024), 0,
                      stream, workspace, blocks, (int)N, dweight, dbias);
   return hipGetLastError();
 }
