@@ -128,10 +128,23 @@ __device__ __forceinline__ T* row_at(T* base, int64_t row, int64_t n, bool bf16)
   return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(base) + row * n * (bf16 ? 2 : 4));
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+
+// Sum over the wave, the same in every lane: over rows of 16 lanes in the vector ALU
+// (each step adds a lane's mirror image, so both have the same sum), then the four
+// rows'.  (Through LDS, as a shuffle goes, each of the six steps waits for it.)
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v = dpp_add<kDppQuadXor1>(v);
+  v = dpp_add<kDppQuadXor2>(v);
+  v = dpp_add<kDppRowHalfMirror>(v);
+  v = dpp_add<kDppRowMirror>(v);
+  auto row = [&](int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+  };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 
 // Sums of K values over the LPR lanes of a row; every lane gets them.  `red`
@@ -148,10 +161,10 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*red)[16]) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float s = 0.f;
+      v4f s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < LPR / 64; ++w) s += red[k][w];
-      v[k] = s;
+      for (int w = 0; w < LPR / 64; w += 4) s += *reinterpret_cast<const v4f*>(&red[k][w]);
+      v[k] = (s[0] + s[1]) + (s[2] + s[3]);
     }
   }
 }
@@ -193,7 +206,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t row, int 
 
 template <bool X_BF16, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_kernel(const NormArgs a) {
-  __shared__ float red[2][1][16];
+  __shared__ __attribute__((aligned(16))) float red[2][1][16];
   constexpr int RPW = kRowThreads<LPR> / LPR;
   const int l = threadIdx.x % LPR;
   const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / LPR;
@@ -271,7 +284,7 @@ struct NormBwArgs {
 
 template <bool X_BF16, bool DY_BF16, int LPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(const NormBwArgs a) {
-  __shared__ float red[2][2][16];
+  __shared__ __attribute__((aligned(16))) float red[2][2][16];
   constexpr int RPW = kRowThreads<LPR> / LPR;
   const int l = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const int N = a.N;
