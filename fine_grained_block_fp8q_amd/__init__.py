@@ -1096,21 +1096,16 @@ def gated_backward(dh, gate_up, act="silu", mode="f32", rows=True, tokens=True, 
     return q, s, qt, st
 
 
-def _norm(wh, x, weight, bias, eps, out_dtype, want_y, codes, mode, stream):
-    if stream is None:
-        native = _native or _compiled()
-        out = (OUT_BF16 if out_dtype is None else _OUT_OF.get(out_dtype)) if want_y else -1
-        if out is not None:
-            r = native.layer_norm(x, weight, bias, eps, out, codes, _MODES[mode])
-            if r is not None:
-                return r if type(r) is not int else _refused(r, wh)
+def _norm(x, weight, bias, eps, y_dtype, codes, mode, stream):
+    """The Python path of both calls below."""
     import torch
+    wh = "fp8q_layer_norm"
     M, N = _dims(wh, x, 2, "x")
     _positive_rows(wh, N)
     if codes:
         _mult128(wh, N=N)
     new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)   # noqa: E731
-    y = new((M, N), out_dtype or torch.bfloat16) if want_y else None
+    y = new((M, N), y_dtype) if y_dtype is not None else None
     q = new((M, N), torch.uint8) if codes else None
     s = new((N // GROUP, M), torch.float32) if codes else None
     mean, rstd = new((M,), torch.float32), new((M,), torch.float32)
@@ -1121,8 +1116,16 @@ def _norm(wh, x, weight, bias, eps, out_dtype, want_y, codes, mode, stream):
 def layer_norm(x, weight, bias=None, eps=1e-5, out_dtype=None, stream=None):
     """(y, mean, rstd): layer norm of the rows of x (float32 or bfloat16 [M][N],
     weight and bias float32 [N]); y is bfloat16 unless out_dtype says float32."""
-    y, _, _, mean, rstd = _norm("fp8q_layer_norm", x, weight, bias, eps, out_dtype, True, False,
-                                "f32", stream)
+    if stream is None:
+        native = _native or _compiled()
+        out = OUT_BF16 if out_dtype is None else _OUT_OF.get(out_dtype)
+        if out is not None:
+            r = native.layer_norm(x, weight, bias, eps, out, False, SCALE_F32)
+            if r is not None:
+                return r if type(r) is not int else _refused(r, "fp8q_layer_norm")
+    import torch
+    y, _, _, mean, rstd = _norm(x, weight, bias, eps, out_dtype or torch.bfloat16, False, "f32",
+                                stream)
     return y, mean, rstd
 
 
@@ -1130,8 +1133,17 @@ def layer_norm_quantized(x, weight, bias=None, eps=1e-5, mode="f32", save_y=Fals
                          stream=None):
     """(q, s, mean, rstd): layer norm written as the E4M3 operand of gemm, from y
     in float32; with save_y, (q, s, mean, rstd, y), y as layer_norm's."""
-    y, q, s, mean, rstd = _norm("fp8q_layer_norm", x, weight, bias, eps, out_dtype, save_y, True,
-                                mode, stream)
+    if stream is None:
+        native = _native or _compiled()
+        out = -1 if not save_y else OUT_BF16 if out_dtype is None else _OUT_OF.get(out_dtype)
+        if out is not None:
+            r = native.layer_norm(x, weight, bias, eps, out, True, _MODES[mode])
+            if r is not None:
+                return r if type(r) is not int else _refused(r, "fp8q_layer_norm")
+    import torch
+    y, q, s, mean, rstd = _norm(x, weight, bias, eps,
+                                (out_dtype or torch.bfloat16) if save_y else None, True, mode,
+                                stream)
     return (q, s, mean, rstd, y) if save_y else (q, s, mean, rstd)
 
 

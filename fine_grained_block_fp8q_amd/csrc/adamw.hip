@@ -24,10 +24,14 @@
 // A workgroup of 256 lanes takes 2048 consecutive elements of one tensor, 16
 // lanes (a DPP row) a group: lane l16 holds elements 4 l16 .. +3 and 64 + 4 l16
 // .. +3 of its group, so that 16 lanes' loads of FP32 are 256 consecutive bytes.
-// Up to kTensors tensors go out in one launch, described in its arguments; a
-// workgroup finds its tensor from the tensors' first workgroups, one a lane.
+// Up to 64 tensors (56 with their scales) go out in one launch, described in its
+// arguments; a workgroup finds its tensor from the tensors' first workgroups, one a
+// lane.  The host writes arguments slowly (a launch alone takes 6 us more for each
+// KiB of them, and 20 more past 4 KiB), so there are launches of 8, 24 and 64.
 
 #include <math.h>
+
+#include <type_traits>
 
 #include "fp8q.h"
 #include "launch.hpp"
@@ -37,18 +41,37 @@ namespace fp8q {
 
 constexpr int kThreads = 256;
 constexpr int kElems = 2048;   // of one workgroup
-constexpr int kTensors = 48;   // of one launch: what 4 KiB of arguments hold
 
-struct AdamwLaunch {
-  fp8q_adamw_tensor t[kTensors];
-  int32_t first[64];  // first workgroup of each tensor; past the last, INT32_MAX
-  const float* lr;    // on the device, or NULL
+struct Moments32 {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  void* copy;
+  int64_t n;
+};
+struct Moments8 : Moments32 {
+  float* m_s;
+  float* v_s;
+};
+template <bool E4M3>
+using Tensor = typename std::conditional<E4M3, Moments8, Moments32>::type;
+
+struct AdamwScalars {
+  const float* lr;  // on the device, or NULL
   const int32_t* step;
   const float* grad_scale;
   double log_b1, log_b2, lr_host, decay;
   float b1, one_b1, b2, one_b2, eps;
   float keep, rate, inv_root;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   uint32_t dither;             // t's part of the dither
+};
+
+template <bool E4M3, int CAP>
+struct AdamwLaunch {
+  AdamwScalars s;
+  int32_t first[CAP];  // first workgroup of each tensor; past the last, INT32_MAX
+  Tensor<E4M3> t[CAP];
 };
 
 constexpr uint32_t kDitherStep = 0x9E3779B1u, kDitherPlace = 0x85EBCA6Bu;
@@ -107,14 +130,15 @@ __device__ __forceinline__ v4f some(int n, F at) {
   return r;
 }
 
-template <bool E4M3_MOMENTS, bool BF16_GRAD>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch a) {
+template <bool E4M3_MOMENTS, bool BF16_GRAD, int CAP>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_MOMENTS, CAP> l) {
+  const AdamwScalars& a = l.s;
   const int lane = threadIdx.x & 63;
   const int bid = (int)blockIdx.x;
-  const uint64_t upto = __ballot(a.first[lane] <= bid);
+  const uint64_t upto = __ballot(lane < CAP && l.first[lane < CAP ? lane : 0] <= bid);
   const int ti = __builtin_amdgcn_readfirstlane(__builtin_popcountll(upto) - 1);
-  const fp8q_adamw_tensor t = a.t[ti];
-  const int64_t base = (int64_t)(bid - a.first[ti]) * kElems;
+  const Tensor<E4M3_MOMENTS> t = l.t[ti];
+  const int64_t base = (int64_t)(bid - l.first[ti]) * kElems;
   const int64_t n = t.n;
 
   float keep = a.keep, rate = a.rate, inv_root = a.inv_root;
@@ -261,9 +285,64 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch a) {
   }
 }
 
+// Tensors tensors[i], tensors[i + 1], ... in one launch, as many as fit; i becomes the
+// first that did not.
+template <bool E4M3, bool BF16_GRAD, int CAP>
+static hipError_t launch(const AdamwScalars& s, const fp8q_adamw_tensor* tensors, int32_t count,
+                         int32_t& i, hipStream_t stream) {
+  AdamwLaunch<E4M3, CAP> a;
+  a.s = s;
+  int k = 0;
+  int64_t blocks = 0;
+  for (; i < count && k < CAP; ++i) {
+    const fp8q_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const int64_t b = (t.n + kElems - 1) / kElems;
+    if (b > max_blocks(kThreads)) return hipErrorInvalidValue;
+    if (blocks + b > max_blocks(kThreads)) break;
+    Tensor<E4M3>& to = a.t[k];
+    to.p = t.p;
+    to.g = t.g;
+    to.m = t.m;
+    to.v = t.v;
+    to.copy = t.copy;
+    to.n = t.n;
+    if constexpr (E4M3) {
+      to.m_s = t.m_s;
+      to.v_s = t.v_s;
+    }
+    a.first[k++] = (int32_t)blocks;
+    blocks += b;
+  }
+  if (k == 0) return hipSuccess;
+  for (int j = k; j < CAP; ++j) {
+    a.first[j] = 0x7FFFFFFF;
+    a.t[j] = Tensor<E4M3>{};
+  }
+  hipLaunchKernelGGL((adamw_kernel<E4M3, BF16_GRAD, CAP>), dim3((unsigned)blocks), dim3(kThreads),
+                     0, stream, a);
+  return hipGetLastError();
+}
+
+template <bool E4M3, bool BF16_GRAD>
+static hipError_t launches(const AdamwScalars& s, const fp8q_adamw_tensor* tensors, int32_t count,
+                           hipStream_t stream) {
+  constexpr int kMost = E4M3 ? 56 : 64;  // of 4 KiB of arguments
+  static_assert(sizeof(AdamwLaunch<E4M3, kMost>) <= 4096, "the arguments of a launch");
+  int32_t i = 0;
+  hipError_t e = hipSuccess;
+  while (i < count && e == hipSuccess) {
+    const int32_t left = count - i;
+    e = left <= 8    ? launch<E4M3, BF16_GRAD, 8>(s, tensors, count, i, stream)
+        : left <= 24 ? launch<E4M3, BF16_GRAD, 24>(s, tensors, count, i, stream)
+                     : launch<E4M3, BF16_GRAD, kMost>(s, tensors, count, i, stream);
+  }
+  return e;
+}
+
 hipError_t launch_adamw(const fp8q_adamw_tensor* tensors, int32_t count, const fp8q_adamw_args& h,
                         int grad_bf16, int e4m3, hipStream_t stream) {
-  AdamwLaunch a;
+  AdamwScalars a;
   a.lr = h.lr_dev;
   a.step = h.step_dev;
   a.grad_scale = h.grad_scale;
@@ -282,28 +361,9 @@ hipError_t launch_adamw(const fp8q_adamw_tensor* tensors, int32_t count, const f
   a.rate = (float)((h.lr_dev ? 1.0 : h.lr) / c1);
   a.inv_root = (float)(1.0 / sqrt(c2));
   a.dither = (uint32_t)h.step * kDitherStep;
-  auto kern = e4m3 ? (grad_bf16 ? adamw_kernel<true, true> : adamw_kernel<true, false>)
-                   : (grad_bf16 ? adamw_kernel<false, true> : adamw_kernel<false, false>);
-  int32_t i = 0;
-  while (i < count) {
-    int k = 0;
-    int64_t blocks = 0;
-    for (; i < count && k < kTensors; ++i) {
-      if (tensors[i].n == 0) continue;
-      const int64_t b = (tensors[i].n + kElems - 1) / kElems;
-      if (b > max_blocks(kThreads)) return hipErrorInvalidValue;
-      if (blocks + b > max_blocks(kThreads)) break;
-      a.t[k] = tensors[i];
-      a.first[k++] = (int32_t)blocks;
-      blocks += b;
-    }
-    if (k == 0) break;
-    for (int j = k; j < 64; ++j) a.first[j] = 0x7FFFFFFF;
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  auto f = e4m3 ? (grad_bf16 ? launches<true, true> : launches<true, false>)
+                : (grad_bf16 ? launches<false, true> : launches<false, false>);
+  return f(a, tensors, count, stream);
 }
 
 }  // namespace fp8q

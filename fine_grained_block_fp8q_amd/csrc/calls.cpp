@@ -284,8 +284,8 @@ fp8q_out_dtype type_code(at::ScalarType t) {
   return t == at::kBFloat16 ? FP8Q_OUT_BF16 : FP8Q_OUT_F32;
 }
 
-// layer_norm(x, weight, bias or None, eps, y's type or -1, codes, mode):
-// (y or None, q or None, s or None, mean, rstd)
+// layer_norm(x, weight, bias or None, eps, y's type or -1, codes, mode): (y, mean,
+// rstd), with codes (q, s, mean, rstd) and y behind them where it is wanted
 PyObject* layer_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   NEEDS(7)
   return guarded([&]() -> PyObject* {
@@ -302,7 +302,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const int out = (int)PyLong_AsLong(args[4]);
     bool codes;
     if (!truth(args[5], codes)) return nullptr;
-    if (!c.ok || N < 1 || N > 16384 || (codes && N % 128)) Py_RETURN_NONE;
+    if (!c.ok || N < 1 || N > 16384 || (codes ? N % 128 != 0 : out < 0)) Py_RETURN_NONE;
     Tensor y, q, s;
     if (out >= 0) y = c.make(out_type(out), {M, N});
     if (codes) {
@@ -310,13 +310,13 @@ PyObject* layer_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       s = c.make(at::kFloat, {N / 128, M});
     }
     const Tensor mean = c.make(at::kFloat, {M}), rstd = c.make(at::kFloat, {M});
-    return answers(
-        entries.layer_norm(at_(*x), type_code(x->scalar_type()), at_<float>(*w),
-                           b ? at_<float>(*b) : nullptr, M, N, (float)PyFloat_AS_DOUBLE(args[3]),
-                           at_(y), out == FP8Q_OUT_BF16 ? FP8Q_OUT_BF16 : FP8Q_OUT_F32,
-                           at_<uint8_t>(q), at_<float>(s), (fp8q_scale_mode)PyLong_AsLong(args[6]),
-                           at_<float>(mean), at_<float>(rstd), c.stream()),
-        y, q, s, mean, rstd);
+    const fp8q_status st = entries.layer_norm(
+        at_(*x), type_code(x->scalar_type()), at_<float>(*w), b ? at_<float>(*b) : nullptr, M, N,
+        (float)PyFloat_AS_DOUBLE(args[3]), at_(y),
+        out == FP8Q_OUT_BF16 ? FP8Q_OUT_BF16 : FP8Q_OUT_F32, at_<uint8_t>(q), at_<float>(s),
+        (fp8q_scale_mode)PyLong_AsLong(args[6]), at_<float>(mean), at_<float>(rstd), c.stream());
+    if (!codes) return answers(st, y, mean, rstd);
+    return y.defined() ? answers(st, q, s, mean, rstd, y) : answers(st, q, s, mean, rstd);
   });
 }
 

@@ -36,14 +36,24 @@ __device__ __forceinline__ ExpertSpan expert_span(const int32_t* off, int G, int
   const int PL = (G + 63) >> 6;  // uniform
   const int e0 = lane * PL;
   constexpr int UP = 4;  // experts whose offsets are loaded together
+  int o0[UP + 1];
+  auto load = [&](int i, int (&o)[UP + 1]) {
+#pragma unroll
+    for (int u = 0; u <= UP; ++u) {
+      const int at = e0 + i + u;
+      o[u] = off[at < G ? at : G];
+    }
+  };
+  load(0, o0);
   // f(expert, its first row, its rows) of the lane's experts, until it says so
   auto each = [&](auto f) {
     for (int i = 0; i < PL; i += UP) {
       int o[UP + 1];
+      if (i == 0) {
 #pragma unroll
-      for (int u = 0; u <= UP; ++u) {
-        const int at = e0 + i + u;
-        o[u] = off[at < G ? at : G];
+        for (int u = 0; u <= UP; ++u) o[u] = o0[u];
+      } else {
+        load(i, o);
       }
 #pragma unroll
       for (int u = 0; u < UP; ++u)

@@ -667,8 +667,9 @@ fp8q_status fp8q_grouped_gemm_rowscaled_precise(const uint8_t* a_q, const float*
   return grouped_rowscaled_call(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out, 1, stream);
 }
 
-// Whether two tensors' p overlap.  A short list is compared pair by pair, a long
-// one in the order of its addresses.
+// Whether two tensors' p overlap.  A list in the order of its addresses (views of one
+// buffer) shows it at once; else a short one is compared pair by pair, a long one
+// sorted.
 static bool p_before(const fp8q_adamw_tensor* a, const fp8q_adamw_tensor* b) {
   return a->n == 0 || b->n == 0 || reinterpret_cast<uintptr_t>(a->p + a->n) <=
                                        reinterpret_cast<uintptr_t>(b->p);
@@ -681,6 +682,14 @@ static int by_p(const void* x, const void* y) {
 }
 
 static fp8q_status check_overlap(const fp8q_adamw_tensor* t, int32_t count) {
+  bool ordered = true;
+  int32_t last = -1;
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    ordered = ordered && (last < 0 || p_before(t + last, t + i));
+    last = i;
+  }
+  if (ordered) return FP8Q_OK;
   if (count <= 64) {
     for (int32_t i = 1; i < count; ++i)
       for (int32_t j = 0; j < i; ++j)

@@ -178,10 +178,17 @@ __device__ __forceinline__ void grouped_rowscaled(
     return;
   }
   __syncthreads();
-  const int x = blockIdx.x % kXcds, step = gridDim.x / kXcds;
-  const int first = __builtin_amdgcn_readfirstlane(run_start(sh.group0, G, tiles, x)) +
-                    (int)(blockIdx.x / kXcds);
-  const int end = __builtin_amdgcn_readfirstlane(run_start(sh.group0, G, tiles, x + 1));
+  // The workgroup's tiles: first, first + step, ... below end.  (A workgroup for every
+  // tile: there are no runs to cut.)
+  const bool all = (int64_t)gridDim.x >= (int64_t)tiles * G;
+  int step = gridDim.x, first = blockIdx.x, end = tiles * G;
+  if (!all) {
+    const int x = blockIdx.x % kXcds;
+    step = gridDim.x / kXcds;
+    first = __builtin_amdgcn_readfirstlane(run_start(sh.group0, G, tiles, x)) +
+            (int)(blockIdx.x / kXcds);
+    end = __builtin_amdgcn_readfirstlane(run_start(sh.group0, G, tiles, x + 1));
+  }
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

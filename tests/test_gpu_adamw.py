@@ -110,7 +110,7 @@ def test_sizes(eight, grad):
             t.check(step)
 
 
-@pytest.mark.parametrize("count", [1, 47, 48, 49, 96, 97, 150])
+@pytest.mark.parametrize("count", [1, 8, 9, 24, 25, 56, 57, 64, 65, 80, 130, 150])
 def test_counts(count):
     """More tensors than one launch describes, empty ones among them."""
     sizes = [(37 * i) % 300 if i % 9 else 0 for i in range(count)]
