@@ -5,29 +5,30 @@
 //   p' = p (1 - lr wd) - lr/(1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps),
 // masters in FP32, moments in FP32 or in 8 bits.  Bound by memory: a master is
 // read and written (8 bytes), the gradient read (2 or 4), the moments read and
-// written (16, or 4 and the scales), the BF16 copy written (2).
+// written (16, or 4 and the scales), the BF16 copy written (2).  44M parameters,
+// moments in FP32, BF16 gradients and copy: 197 us (6.2 TB/s); 342M, moments in 8
+// bits: 935 us (5.9 TB/s), near which the vector ALU's work comes too.
 //
 // Moments in 8 bits: E4M3 codes of m' and of sqrt(v') (the root has half the
 // exponent range of v', so 128 elements of one scale reach 2^35 down from the
 // largest v'), 128 consecutive elements a scale: amax fl(1/448), the codes those of
-// the values times 448 fl(1/amax) (one division a group).  The codes are not rounded to the nearest: a moment moves by a small part of itself
-// a step (5% of v' at b2 = 0.95, 2.5% of its root), less than half of E4M3's
-// step, and would never leave its code.  Each magnitude x is rounded up where
-// its fraction of a step and a dither u reach 1, u = frac(t phi + i psi) in 20
-// bits with i the element's place in its tensor: over the steps of one element
-// the u are spread evenly, so that the codes of a value that stands have its mean.
-// (A moment feeds back into the next step, whose u is related: under a constant
-// gradient the codes' mean is off by 0.3% on average and 1.4% at most, against 0
-// and 1.6% of independent u.)  A root that is not zero keeps a code that is not
-// zero: m' is never divided by eps alone.
+// the values times 448 fl(1/amax) (one division a group).  The codes are not rounded
+// to the nearest: a moment moves by a small part of itself a step (5% of v' at b2 =
+// 0.95, 2.5% of its root), less than half of E4M3's step, and would never leave its
+// code.  Each magnitude x is rounded up where its fraction of a step and a dither u
+// reach 1, u = frac(t phi + i psi) in 20 bits with i the element's place in its
+// tensor: over the steps of one element the u are spread evenly, so that the codes of
+// a value that stands have its mean.  (A moment feeds back into the next step, whose u
+// is related: under a constant gradient the codes' mean is off by 0.3% on average and
+// 1.4% at most, against 0 and 1.6% of independent u.)  A root that is not zero keeps a
+// code that is not zero: m' is never divided by eps alone.
 //
-// A workgroup of 256 lanes takes 2048 consecutive elements of one tensor, 16
-// lanes (a DPP row) a group: lane l16 holds elements 4 l16 .. +3 and 64 + 4 l16
-// .. +3 of its group, so that 16 lanes' loads of FP32 are 256 consecutive bytes.
-// Up to 64 tensors (56 with their scales) go out in one launch, described in its
-// arguments; a workgroup finds its tensor from the tensors' first workgroups, one a
-// lane.  The host writes arguments slowly (a launch alone takes 6 us more for each
-// KiB of them, and 20 more past 4 KiB), so there are launches of 8, 24 and 64.
+// A workgroup of 256 lanes takes 2048 consecutive elements of one tensor, 16 lanes
+// (a DPP row) a group.  Up to 64 tensors (56 with their scales) go out in one launch,
+// described in its arguments; a workgroup finds its tensor from the tensors' first
+// workgroups, one a lane.  The host writes arguments slowly (a launch alone takes 6 us
+// more for each KiB of them, and 20 more past 4 KiB), so there are launches of 8, 24
+// and 64 (60 tensors of 4096 elements: 6.6 us one after the other, 18.4 alone).
 
 #include <math.h>
 
@@ -77,14 +78,25 @@ struct AdamwLaunch {
 constexpr uint32_t kDitherStep = 0x9E3779B1u, kDitherPlace = 0x85EBCA6Bu;
 
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // |x| <= 448 (1 + 2^-23) rounded to E4M3 with the dither's 20 bits u: the step of
 // E4M3 is the 20th bit of an FP32 value; below 2^-6, of the value 2^-6 higher.
 __device__ __forceinline__ float dithered(float x, uint32_t u) {
-  const bool sub = x < 0x1p-6f;
-  const float y = sub ? x + 0x1p-6f : x;
-  const float r = __uint_as_float((__float_as_uint(y) + u) & ~0xFFFFFu);
-  return fminf(sub ? r - 0x1p-6f : r, kE4M3Max);
+  const float up = x < 0x1p-6f ? 0x1p-6f : 0.f;
+  return fminf(__uint_as_float((__float_as_uint(x + up) + u) & ~0xFFFFFu) - up, kE4M3Max);
+}
+
+// The correctly rounded root of x, 0 or at least 2^-96 (below, the products here could
+// lose bits): of the instruction's value, an ulp off at most, and its neighbours the
+// one whose square is nearest.
+__device__ __forceinline__ float root_of_normal(float x) {
+  float s = __builtin_amdgcn_sqrtf(x);
+  const float lo = __uint_as_float(__float_as_uint(s) - 1);
+  const float hi = __uint_as_float(__float_as_uint(s) + 1);
+  const float below = __builtin_fmaf(-lo, s, x), above = __builtin_fmaf(-hi, s, x);
+  s = below <= 0.f ? lo : s;
+  return above > 0.f ? hi : s;
 }
 
 // Scale and multiplier of a group of moments, 0 where the multiplier is not finite.
@@ -97,37 +109,23 @@ __device__ __forceinline__ MomentRule moment_rule(float amax) {
   return {flushed ? 0.f : mul, flushed ? 0.f : amax * (1.f / kE4M3Max)};
 }
 
-template <bool BF16_GRAD>
-__device__ __forceinline__ v4f load_grad(const void* g, int64_t i) {
-  if constexpr (BF16_GRAD) {
-    const v2u w = *reinterpret_cast<const v2u*>(static_cast<const uint16_t*>(g) + i);
-    return v4f{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
-  } else {
-    return *reinterpret_cast<const v4f*>(static_cast<const float*>(g) + i);
-  }
-}
-
-template <bool BF16_GRAD>
-__device__ __forceinline__ float load_grad1(const void* g, int64_t i) {
-  if constexpr (BF16_GRAD)
-    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(g)[i] << 16);
-  else
-    return static_cast<const float*>(g)[i];
-}
+// A lane's eight elements, in two fours.
+struct Eight {
+  v4f v[2];
+};
 
 __device__ __forceinline__ v4f unpack_e4m3x4(uint32_t w) {
   return v4f{__builtin_amdgcn_cvt_f32_fp8((int)w, 0), __builtin_amdgcn_cvt_f32_fp8((int)w, 1),
              __builtin_amdgcn_cvt_f32_fp8((int)w, 2), __builtin_amdgcn_cvt_f32_fp8((int)w, 3)};
 }
 
-// The first `n` (1 .. 4) elements from at; the others 0.
-template <class F>
-__device__ __forceinline__ v4f some(int n, F at) {
-  v4f r = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (j < n) r[j] = at(j);
-  return r;
+__device__ __forceinline__ v4f unpack_bf16x4(uint32_t lo, uint32_t hi) {
+  return v4f{bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
+}
+
+__device__ __forceinline__ v2u pack_bf16x4(const v4f& v) {
+  return v2u{f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16),
+             f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
 }
 
 template <bool E4M3_MOMENTS, bool BF16_GRAD, int CAP>
@@ -139,7 +137,14 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_
   const int ti = __builtin_amdgcn_readfirstlane(__builtin_popcountll(upto) - 1);
   const Tensor<E4M3_MOMENTS> t = l.t[ti];
   const int64_t base = (int64_t)(bid - l.first[ti]) * kElems;
-  const int64_t n = t.n;
+  const int rest = t.n - base < kElems ? (int)(t.n - base) : kElems;  // of the workgroup
+  // (uniform bases, offsets of 32 bits)
+  float* const tp = t.p + base;
+  const float* const g32 = static_cast<const float*>(t.g) + base;
+  const uint16_t* const g16 = static_cast<const uint16_t*>(t.g) + base;
+  float *const m32 = static_cast<float*>(t.m) + base, *const v32 = static_cast<float*>(t.v) + base;
+  uint8_t *const m8 = static_cast<uint8_t*>(t.m) + base, *const v8 = static_cast<uint8_t*>(t.v) + base;
+  uint16_t* const copy = t.copy ? static_cast<uint16_t*>(t.copy) + base : nullptr;
 
   float keep = a.keep, rate = a.rate, inv_root = a.inv_root;
   uint32_t step_dither = a.dither;
@@ -157,67 +162,109 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_
   }
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
 
-  const int l16 = lane & 15;
-  const int64_t group = base + (int64_t)(threadIdx.x >> 4) * kGroup;
-  if (group >= n) return;  // (whole DPP rows)
-  int64_t at[2];
-  int live[2];
-  v4f p[2], g[2], m[2], v[2];
+  // The lane's two fours lie 64 apart, so that 16 lanes' accesses of FP32 are 256
+  // consecutive bytes (eight consecutive elements a lane: 1010 us for 342M parameters
+  // with moments in 8 bits, so 935).
+  const uint32_t l16 = lane & 15, group = (threadIdx.x >> 4) * kGroup;
+  if ((int)group >= rest) return;  // (whole DPP rows)
+  constexpr uint32_t kApart = 64;
+  const uint32_t o = group + 4 * l16;
+  const bool whole = (int)group + kGroup <= rest;
+  auto at = [&](int h, int j) { return o + kApart * h + j; };
+  auto live = [&](int h, int j) { return (int)at(h, j) < rest; };
+  // Streams of 16 bytes a lane, and what is only written, pass the caches by (one layer,
+  // moments in FP32: 197 us; with the gradients' 8 bytes too 204, with none 229).
+  Eight p, g, m, v;
+  if (whole) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    at[h] = group + 64 * h + 4 * l16;
-    const int64_t rest = n - at[h];
-    live[h] = rest >= 4 ? 4 : rest > 0 ? (int)rest : 0;
-    const int64_t i = at[h];
-    if (live[h] == 4) {
-      p[h] = *reinterpret_cast<const v4f*>(t.p + i);
-      g[h] = load_grad<BF16_GRAD>(t.g, i);
-      if constexpr (E4M3_MOMENTS) {
-        m[h] = unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(t.m) + i));
-        v[h] = unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(t.v) + i));
-      } else {
-        m[h] = *reinterpret_cast<const v4f*>(static_cast<float*>(t.m) + i);
-        v[h] = *reinterpret_cast<const v4f*>(static_cast<float*>(t.v) + i);
-      }
+    for (int h = 0; h < 2; ++h)
+      p.v[h] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(tp + at(h, 0)));
+    if constexpr (!BF16_GRAD) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        g.v[h] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(g32 + at(h, 0)));
     } else {
-      const int c = live[h];
-      p[h] = some(c, [&](int j) { return t.p[i + j]; });
-      g[h] = some(c, [&](int j) { return load_grad1<BF16_GRAD>(t.g, i + j); });
-      if constexpr (E4M3_MOMENTS) {
-        auto one = [&](void* b, int j) {
-          return __builtin_amdgcn_cvt_f32_fp8((int)static_cast<uint8_t*>(b)[i + j], 0);
-        };
-        m[h] = some(c, [&](int j) { return one(t.m, j); });
-        v[h] = some(c, [&](int j) { return one(t.v, j); });
-      } else {
-        m[h] = some(c, [&](int j) { return static_cast<float*>(t.m)[i + j]; });
-        v[h] = some(c, [&](int j) { return static_cast<float*>(t.v)[i + j]; });
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v2u w = *reinterpret_cast<const v2u*>(g16 + at(h, 0));
+        g.v[h] = unpack_bf16x4(w[0], w[1]);
       }
     }
+    if constexpr (E4M3_MOMENTS) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m.v[h] = unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(m8 + at(h, 0)));
+        v.v[h] = unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(v8 + at(h, 0)));
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m.v[h] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(m32 + at(h, 0)));
+        v.v[h] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(v32 + at(h, 0)));
+      }
+    }
+  } else {  // the tensor's last group: element by element, zeros past its end
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t i = at(h, j);
+        const bool in = live(h, j);
+        p.v[h][j] = in ? tp[i] : 0.f;
+        g.v[h][j] = !in ? 0.f : BF16_GRAD ? __uint_as_float((uint32_t)g16[i] << 16) : g32[i];
+        if constexpr (E4M3_MOMENTS) {
+          m.v[h][j] = in ? __builtin_amdgcn_cvt_f32_fp8((int)m8[i], 0) : 0.f;
+          v.v[h][j] = in ? __builtin_amdgcn_cvt_f32_fp8((int)v8[i], 0) : 0.f;
+        } else {
+          m.v[h][j] = in ? m32[i] : 0.f;
+          v.v[h][j] = in ? v32[i] : 0.f;
+        }
+      }
   }
+  const int64_t gi = base / kGroup + (threadIdx.x >> 4);
   float ms = 1.f, vs = 1.f;
   if constexpr (E4M3_MOMENTS) {
-    ms = t.m_s[group / kGroup];
-    vs = t.v_s[group / kGroup];
+    ms = t.m_s[gi];
+    vs = t.v_s[gi];
   }
 
-  v4f root[2];
+  Eight root;
+  bool small = false;  // some v is below what root_of_normal() takes
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x = g[h][j] * gs;
-      float m0 = m[h][j], v0 = v[h][j];
+      const float x = g.v[h][j] * gs;
+      float m0 = m.v[h][j], v0 = v.v[h][j];
       if constexpr (E4M3_MOMENTS) {
         m0 = m0 * ms;
         const float r = v0 * vs;
         v0 = r * r;
       }
-      m[h][j] = m0 * a.b1 + x * a.one_b1;
-      v[h][j] = v0 * a.b2 + (x * x) * a.one_b2;
-      root[h][j] = __builtin_sqrtf(v[h][j]);
-      const float den = __builtin_fmaf(root[h][j], inv_root, a.eps);
-      p[h][j] = __builtin_fmaf(p[h][j], keep, -((rate * m[h][j]) / den));
+      m.v[h][j] = m0 * a.b1 + x * a.one_b1;
+      const float vn = v0 * a.b2 + (x * x) * a.one_b2;
+      v.v[h][j] = vn;
+      small = small || (vn < 0x1p-96f && vn != 0.f);
+    }
+  if (__ballot(small) == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) root.v[h][j] = root_of_normal(v.v[h][j]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) root.v[h][j] = __builtin_sqrtf(v.v[h][j]);
+  }
+  // (The update's quotient by the reciprocal instruction, an ulp off at most.)
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float den = __builtin_fmaf(root.v[h][j], inv_root, a.eps);
+      const float quotient = m.v[h][j] * __builtin_amdgcn_rcpf(den);
+      p.v[h][j] = __builtin_fmaf(-rate, quotient, p.v[h][j] * keep);
     }
 
   uint32_t mq[2], vq[2];
@@ -227,17 +274,18 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        am = fmaxf(am, fabsf(m[h][j]));
-        av = fmaxf(av, root[h][j]);
+        am = fmaxf(am, fabsf(m.v[h][j]));
+        av = fmaxf(av, root.v[h][j]);
       }
     const MomentRule rm = moment_rule(row16_max(am)), rv = moment_rule(row16_max(av));
+    const uint32_t place = ((uint32_t)base + o) * kDitherPlace + step_dither;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       v4f cm, cv;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t u = ((uint32_t)(at[h] + j) * kDitherPlace + step_dither) >> 12;
-        const float x = m[h][j] * rm.mul, y = root[h][j] * rv.mul;
+        const uint32_t u = (place + (kApart * h + j) * kDitherPlace) >> 12;
+        const float x = m.v[h][j] * rm.mul, y = root.v[h][j] * rv.mul;
         cm[j] = copysignf(dithered(fabsf(x), u), x);
         const float d = dithered(y, 0xFFFFFu - u);
         cv[j] = d == 0.f && y > 0.f ? 0x1p-9f : d;
@@ -246,42 +294,50 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_
       vq[h] = pack_e4m3x4(cv[0], cv[1], cv[2], cv[3]);
     }
     if (l16 == 0) {
-      t.m_s[group / kGroup] = rm.s;
-      t.v_s[group / kGroup] = rv.s;
+      t.m_s[gi] = rm.s;
+      t.v_s[gi] = rv.s;
     }
   }
 
+  if (whole) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t i = at[h];
-    if (live[h] == 4) {
-      *reinterpret_cast<v4f*>(t.p + i) = p[h];
-      if constexpr (E4M3_MOMENTS) {
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i) = mq[h];
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i) = vq[h];
-      } else {
-        *reinterpret_cast<v4f*>(static_cast<float*>(t.m) + i) = m[h];
-        *reinterpret_cast<v4f*>(static_cast<float*>(t.v) + i) = v[h];
+    for (int h = 0; h < 2; ++h)
+      __builtin_nontemporal_store(p.v[h], reinterpret_cast<v4f*>(tp + at(h, 0)));
+    if constexpr (E4M3_MOMENTS) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<uint32_t*>(m8 + at(h, 0)) = mq[h];
+        *reinterpret_cast<uint32_t*>(v8 + at(h, 0)) = vq[h];
       }
-      if (t.copy)
-        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(t.copy) + i) =
-            v2u{f32_to_bf16_bits(p[h][0]) | (f32_to_bf16_bits(p[h][1]) << 16),
-                f32_to_bf16_bits(p[h][2]) | (f32_to_bf16_bits(p[h][3]) << 16)};
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j >= live[h]) continue;
-        t.p[i + j] = p[h][j];
-        if constexpr (E4M3_MOMENTS) {
-          static_cast<uint8_t*>(t.m)[i + j] = (uint8_t)(mq[h] >> (8 * j));
-          static_cast<uint8_t*>(t.v)[i + j] = (uint8_t)(vq[h] >> (8 * j));
-        } else {
-          static_cast<float*>(t.m)[i + j] = m[h][j];
-          static_cast<float*>(t.v)[i + j] = v[h][j];
-        }
-        if (t.copy) static_cast<uint16_t*>(t.copy)[i + j] = (uint16_t)f32_to_bf16_bits(p[h][j]);
+      for (int h = 0; h < 2; ++h) {
+        __builtin_nontemporal_store(m.v[h], reinterpret_cast<v4f*>(m32 + at(h, 0)));
+        __builtin_nontemporal_store(v.v[h], reinterpret_cast<v4f*>(v32 + at(h, 0)));
       }
     }
+    if (copy) {
+      const v2u lo = pack_bf16x4(p.v[0]), hi = pack_bf16x4(p.v[1]);
+      __builtin_nontemporal_store(lo, reinterpret_cast<v2u*>(copy + at(0, 0)));
+      __builtin_nontemporal_store(hi, reinterpret_cast<v2u*>(copy + at(1, 0)));
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!live(h, j)) continue;
+        const uint32_t i = at(h, j);
+        tp[i] = p.v[h][j];
+        if constexpr (E4M3_MOMENTS) {
+          m8[i] = (uint8_t)(mq[h] >> (8 * j));
+          v8[i] = (uint8_t)(vq[h] >> (8 * j));
+        } else {
+          m32[i] = m.v[h][j];
+          v32[i] = v.v[h][j];
+        }
+        if (copy) copy[i] = (uint16_t)f32_to_bf16_bits(p.v[h][j]);
+      }
   }
 }
 
