@@ -14,9 +14,9 @@ Tolerances (u = 2^-24; each FP32 operation is off by at most u of its result):
   dx     z from the given mean and rstd 2 u |z|, gz = dy w 1 u, both row means 38 u
          + 6 u of the mean of magnitudes and 2 u of the division's; three
          products and differences: 5 u of each term's magnitude.
-  dweight, dbias   a lane's sum over its rows (M/256, or M/4 below 4 * 256 of
-         them), 4 over waves, 256/4 + 4 over workgroups: (M/256 + 80) u of the sum
-         of magnitudes, 3 u of each term's.
+  dweight, dbias   a lane's sum over its rows (at most M/256 + 1 of them), at most
+         16 over the lane groups of a workgroup, at most 1024/32 + 5 over workgroups:
+         below (M/256 + 80) u of the sum of magnitudes, 3 u of each term's.
 """
 
 import numpy as np
@@ -95,6 +95,25 @@ def test_forward(N, dt):
             assert np.all(np.abs(_num(mean) - rm) <= em + 1e-45)
             assert np.all(np.abs(_num(rstd) - rr) <= er)
             assert np.all(np.abs(_num(y) - ry) <= ey + _half(np.abs(ry) + ey, y))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 5, 100, 128, 129, 200, 255, 256, 257])
+def test_narrow_rows_that_share_a_wave(N, dt):
+    """Every number of rows up to two workgroups' of the narrowest, each row as if alone."""
+    rng = np.random.default_rng([N, 4])
+    x, dy = _rows(rng, 33, N, dt), _rows(rng, 33, N, "bf16", 0)
+    w, b = _dev(1 + 0.3 * rng.standard_normal(N)), _dev(rng.standard_normal(N))
+    row = lambda t, i: t[i:i + 1].clone()   # noqa: E731  (a row's own start is not aligned)
+    one = [fq().layer_norm(row(x, i), w, b, 1e-5) for i in range(33)]
+    y, mean, rstd = (torch.cat([o[k] for o in one]) for k in range(3))
+    dx = torch.cat([fq().layer_norm_backward(row(dy, i), row(x, i), w, *one[i][1:])[0]
+                    for i in range(33)])
+    for M in range(1, 34):
+        ym, mm, rm = fq().layer_norm(x[:M], w, b, 1e-5)
+        assert torch.equal(ym, y[:M]) and torch.equal(mm, mean[:M]) and torch.equal(rm, rstd[:M])
+        dm = fq().layer_norm_backward(dy[:M], x[:M], w, mm, rm)
+        assert torch.equal(dm[0], dx[:M])
 
 
 @pytest.mark.parametrize("mode", ["f32", "pow2"])
