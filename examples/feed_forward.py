@@ -10,7 +10,16 @@ E4M3 codes with fine-grained scales:
     backward   gemm (dh), gated_backward (dY along features and along tokens),
                gemm_rowscaled twice (the weight gradients), gemm (dx)
 
-Experts: the same block over routed rows, one call for all experts.
+Experts: the same block over routed rows, one call for all experts; and behind
+a layer norm trained with AdamW, moments in E4M3, its step held in a HIP graph:
+
+    forward    layer_norm_quantized, grouped_gemm_gated, quantize_act,
+               grouped_gemm
+    backward   grouped_gemm (dh), grouped_gated_backward, grouped_quantize_act_t
+               and grouped_gemm_rowscaled (all experts' weight gradients),
+               grouped_gemm (of the norm's output), layer_norm_backward
+    update     adamw_8bit (the experts' weights), adamw (the norm's)
+
 Serving: the trained weights quantized per output channel to int8, activations
 per token; one token at a time and in a batch:
 
@@ -98,6 +107,77 @@ def experts(layers, x, counts):
     return fq.grouped_gemm(*fq.quantize_act(h), off, *stack(w2), out_dtype=BF16)
 
 
+class ExpertLayer:
+    """A layer norm, then G experts' gate, up and down projections: FP32 masters,
+    BF16 copies that the update writes, moments of the matrices in E4M3."""
+
+    def __init__(self, hidden, ffn, n_experts, seed, act="silu"):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        G, rand = n_experts, lambda *s: torch.randn(s, generator=g, device="cuda")   # noqa: E731
+        self.act, self.G = act, G
+        self.norm = [torch.ones(hidden, device="cuda"), torch.zeros(hidden, device="cuda")]
+        self.w = [rand(G, 2 * ffn, hidden) / hidden ** 0.5, rand(G, hidden, ffn) / ffn ** 0.5]
+        self.copies = [w.to(BF16) for w in self.w]
+        zeros = lambda ts, dt: [torch.zeros_like(t, dtype=dt) for t in ts]   # noqa: E731
+        scales = lambda: [torch.zeros(-(-w.numel() // fq.GROUP), device="cuda")   # noqa: E731
+                          for w in self.w]
+        self.moments = (zeros(self.w, torch.uint8), scales(), zeros(self.w, torch.uint8), scales())
+        self.norm_moments = zeros(self.norm, torch.float32), zeros(self.norm, torch.float32)
+        self.step = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def _weights(self, quantize):
+        """[(codes, scales)] of both projections, experts stacked."""
+        return [tuple(torch.stack(t) for t in zip(*[quantize(w) for w in ws]))
+                for ws in self.copies]
+
+    def forward(self, x, off):
+        """x: bf16 [M][hidden], rows grouped by expert -> bf16 [M][hidden]."""
+        w1, w2 = self._weights(fq.quantize_weight)
+        q, s, mean, rstd, n = fq.layer_norm_quantized(x, *self.norm, save_y=True)
+        h, gate_up = fq.grouped_gemm_gated(q, s, off, *w1, act=self.act, save_gate_up=True)
+        self.saved = x, mean, rstd, n, h, gate_up, off
+        return fq.grouped_gemm(*fq.quantize_act(h), off, *w2, out_dtype=BF16)
+
+    def backward(self, dy):
+        """dy: bf16 [M][hidden] -> (dx, [dw1, dw2], [dweight, dbias] of the norm)."""
+        x, mean, rstd, n, h, gate_up, off = self.saved
+        w1, w2 = self._weights(fq.quantize_weight_t)
+        along = lambda t: fq.grouped_quantize_act_t(t, off)   # noqa: E731
+        dh = fq.grouped_gemm(*fq.quantize_act(dy), off, *w2, out_dtype=BF16)
+        dw2 = fq.grouped_gemm_rowscaled(*along(dy), *along(h), off, out_dtype=BF16)
+        q, s, qt, st = fq.grouped_gated_backward(dh, gate_up, off, act=self.act)
+        dw1 = fq.grouped_gemm_rowscaled(qt, st, *along(n), off, out_dtype=BF16)
+        dn = fq.grouped_gemm(q, s, off, *w1, out_dtype=BF16)
+        dx, dweight, dbias = fq.layer_norm_backward(dn, x, self.norm[0], mean, rstd)
+        return dx, [dw1, dw2], [dweight, dbias]
+
+    def update(self, dw, dnorm, lr):
+        self.step += 1
+        fq.adamw_8bit(self.w, dw, *self.moments, self.step, lr=lr, copies=self.copies)
+        fq.adamw(self.norm, dnorm, *self.norm_moments, self.step, lr=lr, weight_decay=0.0)
+
+
+def train_experts(layer, target, x, off, steps, lr):
+    """Fits `layer` to `target` on rows x; one step, captured, is replayed."""
+    hidden = x.shape[1]
+    want = target.forward(x, off).float()
+
+    def step():
+        e = layer.forward(x, off).float() - want
+        _, dw, dnorm = layer.backward((e * (2.0 / hidden)).to(BF16))
+        layer.update(dw, dnorm, lr)
+        return e
+
+    first = float(step().square().mean())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        e = step()
+    for _ in range(steps - 1):
+        graph.replay()
+    return first, float(e.square().mean())
+
+
 def timed(f, n=50):
     for _ in range(5):
         f()
@@ -141,6 +221,11 @@ def main(argv=None):
             worst = max(worst, rel(y[lo:lo + n], l.forward(x[lo:lo + n])))
         lo += n
     print(f"experts in one call: within {worst:.1e} of each expert's own call")
+
+    off = torch.tensor([0, 100, 100, 129, 256], device="cuda", dtype=torch.int32)
+    target, layer = (ExpertLayer(a.hidden, a.ffn, 4, seed) for seed in (20, 21))
+    first, last = train_experts(layer, target, x, off, a.steps, 1e-3)
+    print(f"experts trained with AdamW in 8 bits: loss {first:.4f} -> {last:.4f}")
     return losses
 
 
