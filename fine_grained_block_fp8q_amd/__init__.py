@@ -14,8 +14,9 @@ library then validates sizes, alignment and enums itself.
 
 Allocation helpers (``quantize_act``, ``quantize_weight``, ``gemm``,
 ``grouped_gemm``, ...) allocate outputs with torch on the input's device and
-then call the entry points.  Those of the feed-forward operators
-(``quantize_token_i8``, ``gemm_i8``, ``gemm_gated``, ...) do so in compiled code
+then call the entry points.  Those of the feed-forward operators and of a
+training step (``quantize_token_i8``, ``gemm_i8``, ``gemm_gated``, ...;
+``layer_norm``, ``grouped_gemm_rowscaled``, ``adamw``, ...) do so in compiled code
 (csrc/calls.cpp) when every argument is as it should be and no stream is named;
 else, and where the compiled module cannot be loaded, they take the Python path,
 whose checks say what is wrong.
@@ -190,7 +191,9 @@ def bind(fn, *args, **kwargs):
     finally:
         _capture.on = False
 
-    keep = (args, kwargs)   # the pointers in cargs refer to these tensors' storage
+    # the pointers in cargs refer to these tensors' storage (a list may change later)
+    own = lambda a: tuple(a) if isinstance(a, list) else a   # noqa: E731
+    keep = (tuple(own(a) for a in args), {k: own(a) for k, a in kwargs.items()})
 
     def run():
         st = cfunc(*cargs)
@@ -1163,6 +1166,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, stream=None):
     dbias = new(N, torch.float32) if bias else None
     work = new(layer_norm_backward_workspace(M, N), torch.uint8)
     fp8q_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, work, stream)
+    if stream is not None:      # which may still use it when this returns
+        work.record_stream(stream)
     return dx, dweight, dbias
 
 

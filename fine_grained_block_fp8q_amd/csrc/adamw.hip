@@ -42,6 +42,7 @@ namespace fp8q {
 
 constexpr int kThreads = 256;
 constexpr int kElems = 2048;   // of one workgroup
+static_assert((int64_t(1) << 34) / kElems <= max_blocks(kThreads), "the largest tensor in a launch");
 
 struct Moments32 {
   float* p;
@@ -354,7 +355,6 @@ static hipError_t launch(const AdamwScalars& s, const fp8q_adamw_tensor* tensors
     const fp8q_adamw_tensor& t = tensors[i];
     if (t.n == 0) continue;
     const int64_t b = (t.n + kElems - 1) / kElems;
-    if (b > max_blocks(kThreads)) return hipErrorInvalidValue;
     if (blocks + b > max_blocks(kThreads)) break;
     Tensor<E4M3>& to = a.t[k];
     to.p = t.p;

@@ -738,6 +738,8 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int32_t count,
       !not_negative(args->weight_decay) || !(args->beta1 >= 0.0 && args->beta1 < 1.0) ||
       !(args->beta2 >= 0.0 && args->beta2 < 1.0) || (!args->step_dev && args->step < 1))
     return FP8Q_ERR_UNSUPPORTED;
+  for (int32_t i = 0; i < count; ++i)
+    if (tensors[i].n > (int64_t(1) << 34)) return FP8Q_ERR_UNSUPPORTED;  // one launch's
   if (work == 0) return FP8Q_OK;
   const fp8q_status o = check_overlap(tensors, count);
   if (o != FP8Q_OK) return o;

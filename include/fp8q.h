@@ -23,7 +23,8 @@
  *
  * Conventions for every call:
  *   - Every data pointer is a DEVICE pointer on the current HIP device.  The
- *     caller allocates and frees all memory; the library allocates nothing,
+ *     caller allocates and frees all memory; the library allocates nothing (but
+ *     host memory during a call: fp8q_adamw, to sort more than 64 tensors),
  *     keeps no pointer after returning, creates no stream and never
  *     synchronizes.  Work is enqueued on `stream` (NULL = the default stream)
  *     and runs asynchronously.
@@ -611,7 +612,7 @@ typedef struct {
   float* m_s;     /* scales of m and v: E4M3 moments only                           */
   float* v_s;
   void* copy;     /* p as bfloat16 [n] (output), or NULL                            */
-  int64_t n;      /* elements; 0: nothing to do                                     */
+  int64_t n;      /* elements, at most 2^34; 0: nothing to do                       */
 } fp8q_adamw_tensor;
 
 typedef struct {
@@ -627,8 +628,8 @@ typedef struct {
  *   All data pointers 16-byte aligned, scales and the device scalars 4-byte.
  * A captured call keeps host values: a graph that is replayed step after step takes
  * its step's number (and a changing lr) from the device.
- * FP8Q_ERR_UNSUPPORTED: two tensors' p overlap, a beta outside [0, 1), lr, eps or
- * weight_decay negative or not finite, or step < 1 (without step_dev).
+ * FP8Q_ERR_UNSUPPORTED: two tensors' p overlap, n > 2^34, a beta outside [0, 1), lr,
+ * eps or weight_decay negative or not finite, or step < 1 (without step_dev).
  * No other memory of one call may overlap.
  */
 fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int32_t count,

@@ -187,3 +187,45 @@ def test_flags_whose_truth_cannot_be_told(calls, flag):
 def test_save_y_whose_truth_cannot_be_told(calls, name):
     with pytest.raises(ValueError, match="ambiguous"):
         calls[name][0](save_y=np.array([1, 0]))
+
+
+def test_a_workspace_stays_taken_while_a_given_stream_uses_it(monkeypatch):
+    """The workspace of a call on a stream that is behind is not handed out again."""
+    f = fq()
+    x = torch.randn(2000, 1024, device=DEV)
+    w = torch.randn(1024, device=DEV)
+    _, mean, rstd = f.layer_norm(x, w)
+    entry, seen = f.fp8q_layer_norm_backward, []
+
+    def spy(*args):
+        seen.append((args[8].data_ptr(), args[8].numel()))
+        entry(*args)
+
+    monkeypatch.setattr(f, "fp8q_layer_norm_backward", spy)
+    want = f.layer_norm_backward(x, x, w, mean, rstd)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)       # some 50 ms
+    got = f.layer_norm_backward(x, x, w, mean, rstd, stream=side)
+    taken = [torch.empty(seen[-1][1], dtype=torch.uint8, device=DEV) for _ in range(4)]
+    waiting = not side.query()
+    side.synchronize()
+    assert waiting and seen[-1][0] not in [t.data_ptr() for t in taken]
+    assert _same(got, want)
+
+
+def test_a_bound_call_holds_its_lists_tensors():
+    f = fq()
+    lists = [[torch.randn(512, device=DEV)] for _ in range(2)] + \
+        [[torch.zeros(512, device=DEV)] for _ in range(2)]
+    p, others = lists[0][0], [l[0].data_ptr() for l in lists[1:]]
+    run = f.bind(f.fp8q_adamw, *lists, 1)
+    for l in lists:
+        l.clear()
+    again = [torch.empty(512, device=DEV).data_ptr() for _ in range(8)]
+    assert not set(others) & set(again)
+    before = p.clone()
+    run()
+    assert not torch.equal(p, before)

@@ -237,6 +237,7 @@ def test_adamw_refusals(lib):
     assert _adamw(lib, [dict(copy=A + 8)]) == E_ALIGN
     assert _adamw(lib, count=-1) == E_SHAPE
     assert _adamw(lib, [dict(n=-1)]) == E_SHAPE
+    assert _adamw(lib, [{}, dict(n=2 ** 34 + 1)], count=2) == E_UNSUP
     for n in ("lr_dev", "step_dev", "grad_scale"):
         assert _adamw(lib, **{n: A + 2}) == E_ALIGN
     assert _adamw(lib, grad=2) == E_ENUM and _adamw(lib, moments=2) == E_ENUM
