@@ -9,6 +9,8 @@
 // group's rows from off takes as long as a piece).  As in quantize_act_t, a column's
 // maximum goes over the lane's 4 rows, the wave and the 4 waves, and the codes
 // through a transposed copy in LDS.  Bound by memory (2 bytes read, 1 written).
+// 32768 tokens of 256 experts, K = 7168: 217 us (953 MB with the zeros, 4.4 TB/s; one
+// piece a workgroup 298); 512 tokens of 8, K = 2048: 5.6 us, a launch.
 
 #include "experts.hpp"
 #include "fp8q.h"

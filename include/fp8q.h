@@ -583,7 +583,8 @@ fp8q_status fp8q_grouped_gemm_rowscaled_precise(const uint8_t* a_q, const float*
  *   m = fl(fl(beta1 m) + fl((1 - beta1) g)),
  *   v = fl(fl(beta2 v) + fl((1 - beta2) fl(g g))),
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps);
- * the factors of lr, weight_decay and t are formed in 64 bits and rounded once.
+ * the factors of lr, weight_decay and t are formed in 64 bits and rounded once, and p
+ * is within 2^-24 (3 |p| + 8 |update|) of the formula with these m and v.
  *
  * Moments in E4M3 (FP8Q_MOMENTS_E4M3): m holds codes of m and v codes of r = sqrt(v),
  * each 128 consecutive elements of a tensor (the last ones fewer) with one scale,

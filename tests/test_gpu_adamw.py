@@ -1,9 +1,9 @@
 """AdamW on the GPU.  Moments and their codes and scales are held bit for bit to the
 call's FP32 operations (oracle.training_step).  The new parameter is held to
 float64 from those moments: p (1 - lr wd) with a rounded factor, product and
-difference 3 u |p|; the update is three rounded factors, a product, a quotient and
-a root's product and sum, each within u (the root itself half a unit), and one
-more for the difference: 8 u of it; half an ulp of BF16 (2^-8) for the copy."""
+difference 3 u |p|; the update has two rounded factors, a root, the denominator's
+sum and a product, each within u, a reciprocal within an ulp (2 u), and one more for
+the difference: 8 u of it; half an ulp of BF16 (2^-8) for the copy."""
 
 import numpy as np
 import pytest
