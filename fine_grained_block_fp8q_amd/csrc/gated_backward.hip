@@ -38,6 +38,10 @@
 // By expert (EXPERTS): the groups of tokens are those of experts.hpp, of which each
 // expert's last one may end early; everything else is the same.  Rows past the
 // last expert are in no group, and their codes along the features not written.
+// Finding a group's rows takes as long as a fifth of a block, so a workgroup takes
+// several blocks of features; waves without tokens and groups that there are not are
+// spared the work.  F = 2048, us, before and after: 8192 tokens of 32 experts 45.6 and
+// 41, 32768 of 256 (groups two thirds full) 260 and 205, 2000 of 64 32 and 20.6.
 
 #include <type_traits>
 
@@ -58,6 +62,9 @@ constexpr int kBwThreads = 512;
 // own, of 16 tokens (rows' form) and 32 features (tokens' form).
 constexpr int kRowsTokens = 16, kTokensFeatures = 32, kSmallThreads = 256;
 constexpr int64_t kSmallBlocks = 128;
+// By expert a workgroup takes up to kBwBlocks blocks of features, as many as leave
+// kBwWorkgroups of them.
+constexpr int64_t kBwBlocks = 4, kBwWorkgroups = 2048;
 
 __device__ __forceinline__ float bf16_elem(const uint4& v, int j) {
   const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
@@ -131,7 +138,7 @@ struct BwShared {
 };
 
 // Group of tokens tb: its first row mb and its number of rows `live`.
-template <int MODE, int ACT>
+template <int MODE, int ACT, bool EXPERTS>
 __device__ __forceinline__ void gated_backward(
     const uint16_t* dh, const uint16_t* gu, int64_t M, int64_t F, uint8_t* q, float* s, uint8_t* qt,
     float* st, int64_t Mp, int fb, int64_t tb, int64_t mb, int live, BwShared& sh) {
@@ -153,12 +160,21 @@ __device__ __forceinline__ void gated_backward(
     vu[i] = load16(ry, aty + (uint32_t)fs * 2);
   }
   float d[2][4][8];  // dgate, dup
+  // (an expert's last group may have few tokens: waves without any are spared the work)
+  const bool some = !EXPERTS || 16 * __builtin_amdgcn_readfirstlane(wave) < live;
+  if (some) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) gate_up_grad<ACT>(vd[i], vg[i], vu[i], j, d[0][i][j], d[1][i][j]);
+      for (int j = 0; j < 8; ++j) gate_up_grad<ACT>(vd[i], vg[i], vu[i], j, d[0][i][j], d[1][i][j]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[0][i][j] = d[1][i][j] = 0.f;
+  }
 
-  if (q) {
+  if (q && some) {
     // lane l16 < 8 of a DPP row: the group of half l16/4, token 4rq + l16%4
     float amax = 0.f;
 #pragma unroll
@@ -242,23 +258,47 @@ __device__ __forceinline__ void gated_backward(
   }
 }
 
+// The tokens' form of a group that there is not: zeros.
+__device__ __forceinline__ void no_tokens(int64_t F, uint8_t* qt, float* st, int64_t Mp, int fb0,
+                                          int fb_end, int64_t tb) {
+  const int t = threadIdx.x, n = (fb_end - fb0) * kGroup;
+  for (int h = 0; h < 2; ++h) {
+    const int64_t c0 = h * F + (int64_t)fb0 * kGroup;
+    for (int c = t >> 3; c < n; c += kBwThreads / 8)
+      __builtin_nontemporal_store(v4u{0, 0, 0, 0}, reinterpret_cast<v4u*>(
+                                      qt + (c0 + c) * Mp + tb * kGroup + 16 * (t & 7)));
+    for (int c = t; c < n; c += kBwThreads) st[tb * 2 * F + c0 + c] = 0.f;
+  }
+}
+
 template <int MODE, int ACT, bool EXPERTS>
 __global__ __launch_bounds__(kBwThreads) void gated_backward_kernel(
     const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu, int64_t M, int64_t F,
     const int32_t* __restrict__ off, int G, uint8_t* __restrict__ q, float* __restrict__ s,
-    uint8_t* __restrict__ qt, float* __restrict__ st, int64_t Mp, int n_fblk) {
+    uint8_t* __restrict__ qt, float* __restrict__ st, int64_t Mp, int n_fblk, int blocks) {
   __shared__ __attribute__((aligned(16))) BwShared sh;
-  const int fb = blockIdx.x % n_fblk;
-  const int64_t tb = blockIdx.x / n_fblk;
-  int64_t mb = tb * kGroup;
-  int live = __builtin_amdgcn_readfirstlane(M - mb < kGroup ? (int)(M - mb) : kGroup);
   if constexpr (EXPERTS) {
+    const int n_chunk = (n_fblk + blocks - 1) / blocks;
+    const int fb0 = (int)(blockIdx.x % n_chunk) * blocks;
+    const int64_t tb = blockIdx.x / n_chunk;
+    const int fb_end = fb0 + blocks < n_fblk ? fb0 + blocks : n_fblk;
     const ExpertSpan span = expert_span<true>(off, G, M, Mp / kGroup, (int)tb);
     if (invalid(span)) return;
-    mb = span.first;
-    live = span.rows;
+    if (span.rows == 0) {  // past the last group: zeros
+      if (qt) no_tokens(F, qt, st, Mp, fb0, fb_end, tb);
+      return;
+    }
+    // (no barrier between blocks: the last one reads the tile, which the next one
+    // writes behind two of its own)
+    for (int fb = fb0; fb < fb_end; ++fb)
+      gated_backward<MODE, ACT, true>(dh, gu, M, F, q, s, qt, st, Mp, fb, tb, span.first,
+                                      span.rows, sh);
+  } else {
+    const int fb = blockIdx.x % n_fblk;
+    const int64_t tb = blockIdx.x / n_fblk, mb = tb * kGroup;
+    const int live = __builtin_amdgcn_readfirstlane(M - mb < kGroup ? (int)(M - mb) : kGroup);
+    gated_backward<MODE, ACT, false>(dh, gu, M, F, q, s, qt, st, Mp, fb, tb, mb, live, sh);
   }
-  gated_backward<MODE, ACT>(dh, gu, M, F, q, s, qt, st, Mp, fb, tb, mb, live, sh);
 }
 
 // ---- few groups: each form by workgroups of its own, in small pieces
@@ -421,9 +461,12 @@ static hipError_t launch(const void* dh, const void* gu, int64_t M, const int32_
                                            : gated_backward_kernel<1, kActSilu, EXPERTS>)
                               : (mode == 0 ? gated_backward_kernel<0, kActGeluTanh, EXPERTS>
                                            : gated_backward_kernel<1, kActGeluTanh, EXPERTS>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(n_fblk * tb)), dim3(kBwThreads), 0, stream,
+  int64_t blocks = EXPERTS ? n_fblk * tb / kBwWorkgroups : 1;
+  blocks = blocks < 1 ? 1 : blocks > kBwBlocks ? kBwBlocks : blocks;
+  const int64_t n_chunk = (n_fblk + blocks - 1) / blocks;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(n_chunk * tb)), dim3(kBwThreads), 0, stream,
                      static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(gu), M, F, off,
-                     G, q, s, qt, st, tb * kGroup, (int)n_fblk);
+                     G, q, s, qt, st, tb * kGroup, (int)n_fblk, (int)blocks);
   return hipGetLastError();
 }
 

@@ -285,3 +285,32 @@ def test_debug_build_reports_invalid_offsets():
             assert r == r2 == OK, name
             for a, b in zip(outs, outs2):
                 assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("mode", ["f32", "pow2"])
+def test_grouped_gated_backward_of_many_groups_is_each_experts_own(mode):
+    """Enough groups that a workgroup takes several blocks of features, the last one fewer:
+    every expert's codes are those of a call for it alone, bit for bit."""
+    G, F, M = 200, 17 * 128, 20000
+    rng = np.random.default_rng(12)
+    counts = rng.integers(0, 150, size=G)
+    counts[[0, 7, 199]] = 0, 700, 0
+    off = np.concatenate([[0], np.cumsum(counts)])
+    assert off[-1] < M
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    dh = torch.randn((M, F), generator=g, device=DEV).to(torch.bfloat16)
+    gu = torch.randn((M, 2 * F), generator=g, device=DEV).to(torch.bfloat16)
+    offd = torch.from_numpy(off.astype(np.int32)).to(DEV)
+    q, s, qt, st = fq().grouped_gated_backward(dh, gu, offd, mode=mode)
+    at = 0
+    for e in range(G):
+        lo, hi = int(off[e]), int(off[e + 1])
+        n = -(-(hi - lo) // 128)
+        if n:
+            eq, es, eqt, est = fq().gated_backward(dh[lo:hi].clone(), gu[lo:hi].clone(), mode=mode)
+            assert torch.equal(q[lo:hi], eq) and torch.equal(s[:, lo:hi], es), e
+            assert torch.equal(qt[:, 128 * at:128 * (at + n)], eqt), e
+            assert torch.equal(st[at:at + n], est), e
+        at += n
+    assert not qt[:, 128 * at:].any() and not st[at:].any()
