@@ -14,7 +14,9 @@ library then validates sizes, alignment and enums itself.
 
 Allocation helpers (``quantize_act``, ``quantize_weight``, ``gemm``,
 ``grouped_gemm``, ...) allocate outputs with torch on the input's device and
-then call the entry points.  Those of the feed-forward operators and of a
+then call the entry points.  Given a ``stream``, they allocate on it; the caller
+orders the inputs before the call and its own use of the outputs behind it, and
+keeps the inputs until it has run (the outputs may be dropped at any time).  Those of the feed-forward operators and of a
 training step (``quantize_token_i8``, ``gemm_i8``, ``gemm_gated``, ...;
 ``layer_norm``, ``grouped_gemm_rowscaled``, ``adamw``, ...) do so in compiled code
 (csrc/calls.cpp) when every argument is as it should be and no stream is named;
@@ -868,11 +870,38 @@ def fp8q_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 
 
 
 # ---------------------------------------------------------- allocation helpers
+def _new(stream, device, *wanted):
+    """Tensors of the (shape, dtype) pairs, None for a None, that a call on `stream`
+    (None: the current one) writes.
+
+    torch hands a freed block out again to the stream it was allocated on, whose order
+    keeps the old use before the new.  So a named stream's tensors are allocated on
+    that stream: a block of the current one's may be in use by work of its that is
+    still pending.  The caller goes on with them on the current stream: it is recorded,
+    and a block that is dropped waits for what the current stream does with it."""
+    import torch
+
+    def made():
+        return [w and torch.empty(w[0], dtype=w[1], device=device) for w in wanted]
+    if stream is None or device.type != "cuda":
+        return made()
+    here = torch.cuda.current_stream(device)
+    if stream.cuda_stream == here.cuda_stream:
+        return made()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        tensors = made()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(here)
+    return tensors
+
+
 def quantize_act(x, mode="f32", stream=None):
     import torch
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    s = torch.empty((K // GROUP, M), dtype=torch.float32, device=x.device)
+    q, s = _new(stream, x.device, ((M, K), torch.uint8), ((K // GROUP, M), torch.float32))
     fp8q_quantize_act(x, q, s, mode, stream)
     return q, s
 
@@ -880,8 +909,7 @@ def quantize_act(x, mode="f32", stream=None):
 def quantize_weight(w, mode="f32", stream=None):
     import torch
     N, K = w.shape
-    q = torch.empty((N, K), dtype=torch.uint8, device=w.device)
-    s = torch.empty((N // GROUP, K // GROUP), dtype=torch.float32, device=w.device)
+    q, s = _new(stream, w.device, ((N, K), torch.uint8), ((N // GROUP, K // GROUP), torch.float32))
     fp8q_quantize_weight(w, q, s, mode, stream)
     return q, s
 
@@ -889,8 +917,7 @@ def quantize_weight(w, mode="f32", stream=None):
 def quantize_act_t(x, mode="f32", stream=None):
     import torch
     M, K = x.shape
-    q = torch.empty((K, M), dtype=torch.uint8, device=x.device)
-    s = torch.empty((M // GROUP, K), dtype=torch.float32, device=x.device)
+    q, s = _new(stream, x.device, ((K, M), torch.uint8), ((M // GROUP, K), torch.float32))
     fp8q_quantize_act_t(x, q, s, mode, stream)
     return q, s
 
@@ -898,8 +925,7 @@ def quantize_act_t(x, mode="f32", stream=None):
 def quantize_weight_t(w, mode="f32", stream=None):
     import torch
     N, K = w.shape
-    q = torch.empty((K, N), dtype=torch.uint8, device=w.device)
-    s = torch.empty((K // GROUP, N // GROUP), dtype=torch.float32, device=w.device)
+    q, s = _new(stream, w.device, ((K, N), torch.uint8), ((K // GROUP, N // GROUP), torch.float32))
     fp8q_quantize_weight_t(w, q, s, mode, stream)
     return q, s
 
@@ -907,7 +933,7 @@ def quantize_weight_t(w, mode="f32", stream=None):
 def gemm_rowscaled(a_q, a_s, b_q, b_s, out_dtype=None, stream=None, precise=False):
     import torch
     out_dtype = out_dtype or torch.float32
-    c = torch.empty((a_q.shape[0], b_q.shape[0]), dtype=out_dtype, device=a_q.device)
+    (c,) = _new(stream, a_q.device, ((a_q.shape[0], b_q.shape[0]), out_dtype))
     f = fp8q_gemm_rowscaled_precise if precise else fp8q_gemm_rowscaled
     f(a_q, a_s, b_q, b_s, c, stream)
     return c
@@ -916,7 +942,7 @@ def gemm_rowscaled(a_q, a_s, b_q, b_s, out_dtype=None, stream=None, precise=Fals
 def gemm(a_q, a_s, w_q, w_s, out_dtype=None, stream=None, precise=False, mfma_scaled=False):
     import torch
     out_dtype = out_dtype or torch.float32
-    c = torch.empty((a_q.shape[0], w_q.shape[0]), dtype=out_dtype, device=a_q.device)
+    (c,) = _new(stream, a_q.device, ((a_q.shape[0], w_q.shape[0]), out_dtype))
     assert not (precise and mfma_scaled), "one GEMM mode"
     f = fp8q_gemm_precise if precise else fp8q_gemm_mfma_scaled if mfma_scaled else fp8q_gemm
     f(a_q, a_s, w_q, w_s, c, stream)
@@ -926,7 +952,7 @@ def gemm(a_q, a_s, w_q, w_s, out_dtype=None, stream=None, precise=False, mfma_sc
 def gemm_fused(x, w_q, w_s, mode="f32", out_dtype=None, stream=None):
     import torch
     out_dtype = out_dtype or torch.float32
-    c = torch.empty((x.shape[0], w_q.shape[0]), dtype=out_dtype, device=x.device)
+    (c,) = _new(stream, x.device, ((x.shape[0], w_q.shape[0]), out_dtype))
     fp8q_gemm_fused(x, w_q, w_s, c, mode, stream)
     return c
 
@@ -934,7 +960,7 @@ def gemm_fused(x, w_q, w_s, mode="f32", out_dtype=None, stream=None):
 def grouped_gemm_fused(x, off, w_q, w_s, mode="f32", out_dtype=None, stream=None):
     import torch
     out_dtype = out_dtype or torch.float32
-    c = torch.empty((x.shape[0], w_q.shape[1]), dtype=out_dtype, device=x.device)
+    (c,) = _new(stream, x.device, ((x.shape[0], w_q.shape[1]), out_dtype))
     fp8q_grouped_gemm_fused(x, off, w_q, w_s, c, mode, stream)
     return c
 
@@ -942,7 +968,7 @@ def grouped_gemm_fused(x, off, w_q, w_s, mode="f32", out_dtype=None, stream=None
 def grouped_gemm(a_q, a_s, off, w_q, w_s, out_dtype=None, stream=None, precise=False):
     import torch
     out_dtype = out_dtype or torch.float32
-    c = torch.empty((a_q.shape[0], w_q.shape[1]), dtype=out_dtype, device=a_q.device)
+    (c,) = _new(stream, a_q.device, ((a_q.shape[0], w_q.shape[1]), out_dtype))
     f = fp8q_grouped_gemm_precise if precise else fp8q_grouped_gemm
     f(a_q, a_s, off, w_q, w_s, c, stream)
     return c
@@ -1002,8 +1028,7 @@ def quantize_token_i8(x, stream=None):
             return r if type(r) is not int else _refused(r, wh)
     import torch
     M, K = _dims(wh, x, 2, "x")
-    q = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=x.device)
-    s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    q, s = _new(stream, x.device, ((M, -(-K // 16) * 16), torch.int8), ((M,), torch.float32))
     fp8q_quantize_token_i8(x, q, s, stream)
     return q, s
 
@@ -1019,7 +1044,7 @@ def gemm_i8(a_q, a_s, w_q, w_s, bias=None, out_dtype=None, stream=None):
                 return r if type(r) is not int else _refused(r, wh)
     import torch
     M, N = _rows(wh, a_q, w_q)
-    c = torch.empty((M, N), dtype=out_dtype or torch.float32, device=a_q.device)
+    (c,) = _new(stream, a_q.device, ((M, N), out_dtype or torch.float32))
     fp8q_gemm_i8(a_q, a_s, w_q, w_s, c, bias, stream)
     return c
 
@@ -1036,7 +1061,7 @@ def gemm_i8_gated(a_q, a_s, w_q, w_s, act="silu", out_dtype=None, stream=None):
                 return r if type(r) is not int else _refused(r, wh)
     import torch
     M, N = _rows(wh, a_q, w_q)
-    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
+    (h,) = _new(stream, a_q.device, ((M, N // 2), out_dtype or torch.bfloat16))
     fp8q_gemm_i8_gated(a_q, a_s, w_q, w_s, h, act, stream)
     return h
 
@@ -1052,8 +1077,8 @@ def _gated(wh, a_q, a_s, off, w_q, w_s, act, out_dtype, save_gate_up, stream):
     import torch
     M = _dims(wh, a_q, 2, "a_q")[0]
     N = _dims(wh, w_q, 2 if off is None else 3, "w_q")[-2]
-    h = torch.empty((M, N // 2), dtype=out_dtype or torch.bfloat16, device=a_q.device)
-    gu = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device) if save_gate_up else None
+    h, gu = _new(stream, a_q.device, ((M, N // 2), out_dtype or torch.bfloat16),
+                 ((M, N), torch.bfloat16) if save_gate_up else None)
     if off is None:
         fp8q_gemm_gated(a_q, a_s, w_q, w_s, h, act, gu, stream)
     else:
@@ -1075,6 +1100,15 @@ def grouped_gemm_gated(a_q, a_s, off, w_q, w_s, act="silu", out_dtype=None, save
     return _gated(wh, a_q, a_s, off, w_q, w_s, act, out_dtype, save_gate_up, stream)
 
 
+def _both_forms(stream, device, M, F, groups, rows, tokens):
+    """q, s, qt, st of the gated block's backward pass, of M rows and `groups` of tokens."""
+    import torch
+    return _new(stream, device, ((M, 2 * F), torch.uint8) if rows else None,
+                ((2 * F // GROUP, M), torch.float32) if rows else None,
+                ((2 * F, groups * GROUP), torch.uint8) if tokens else None,
+                ((groups, 2 * F), torch.float32) if tokens else None)
+
+
 def gated_backward(dh, gate_up, act="silu", mode="f32", rows=True, tokens=True, stream=None):
     """(q, s, qt, st): dY in E4M3 along the features and along the tokens, for
     gemm (dX = dY W) and gemm_rowscaled (dW = dY^T X).  rows=False or
@@ -1085,16 +1119,8 @@ def gated_backward(dh, gate_up, act="silu", mode="f32", rows=True, tokens=True, 
                                                     tokens)
         if r is not None:
             return r if type(r) is not int else _refused(r, wh)
-    import torch
     M, F = _dims(wh, dh, 2, "dh")
-    dev, groups = dh.device, -(-M // GROUP)
-    q = s = qt = st = None
-    if rows:
-        q = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
-        s = torch.empty((2 * F // GROUP, M), dtype=torch.float32, device=dev)
-    if tokens:
-        qt = torch.empty((2 * F, groups * GROUP), dtype=torch.uint8, device=dev)
-        st = torch.empty((groups, 2 * F), dtype=torch.float32, device=dev)
+    q, s, qt, st = _both_forms(stream, dh.device, M, F, -(-M // GROUP), rows, tokens)
     fp8q_gated_backward(dh, gate_up, q, s, qt, st, act, mode, stream)
     return q, s, qt, st
 
@@ -1107,11 +1133,10 @@ def _norm(x, weight, bias, eps, y_dtype, codes, mode, stream):
     _positive_rows(wh, N)
     if codes:
         _mult128(wh, N=N)
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)   # noqa: E731
-    y = new((M, N), y_dtype) if y_dtype is not None else None
-    q = new((M, N), torch.uint8) if codes else None
-    s = new((N // GROUP, M), torch.float32) if codes else None
-    mean, rstd = new((M,), torch.float32), new((M,), torch.float32)
+    y, q, s, mean, rstd = _new(
+        stream, x.device, ((M, N), y_dtype) if y_dtype is not None else None,
+        ((M, N), torch.uint8) if codes else None, ((N // GROUP, M), torch.float32) if codes else None,
+        ((M,), torch.float32), ((M,), torch.float32))
     fp8q_layer_norm(x, weight, bias, mean, rstd, y, q, s, eps, mode, stream)
     return y, q, s, mean, rstd
 
@@ -1160,14 +1185,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, stream=None):
             return r if type(r) is not int else _refused(r, wh)
     import torch
     M, N = _dims(wh, x, 2, "x")
-    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-    new = lambda n, dt: torch.empty((n,), dtype=dt, device=x.device)   # noqa: E731
-    dweight = new(N, torch.float32)
-    dbias = new(N, torch.float32) if bias else None
-    work = new(layer_norm_backward_workspace(M, N), torch.uint8)
+    dx, dweight, dbias, work = _new(
+        stream, x.device, ((M, N), x.dtype), ((N,), torch.float32),
+        ((N,), torch.float32) if bias else None, ((layer_norm_backward_workspace(M, N),), torch.uint8))
     fp8q_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, work, stream)
-    if stream is not None:      # which may still use it when this returns
-        work.record_stream(stream)
     return dx, dweight, dbias
 
 
@@ -1183,8 +1204,7 @@ def grouped_quantize_act_t(x, off, mode="f32", stream=None):
     import torch
     M, K = _dims(wh, x, 2, "x")
     T = expert_columns(M, _offsets(wh, off, x.device))
-    q = torch.empty((K, T), dtype=torch.uint8, device=x.device)
-    s = torch.empty((T // GROUP, K), dtype=torch.float32, device=x.device)
+    q, s = _new(stream, x.device, ((K, T), torch.uint8), ((T // GROUP, K), torch.float32))
     fp8q_grouped_quantize_act_t(x, off, q, s, mode, stream)
     return q, s
 
@@ -1199,17 +1219,9 @@ def grouped_gated_backward(dh, gate_up, off, act="silu", mode="f32", rows=True, 
                                                             _MODES[mode], rows, tokens)
         if r is not None:
             return r if type(r) is not int else _refused(r, wh)
-    import torch
     M, F = _dims(wh, dh, 2, "dh")
-    dev = dh.device
-    T = expert_columns(M, _offsets(wh, off, dev))
-    q = s = qt = st = None
-    if rows:
-        q = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
-        s = torch.empty((2 * F // GROUP, M), dtype=torch.float32, device=dev)
-    if tokens:
-        qt = torch.empty((2 * F, T), dtype=torch.uint8, device=dev)
-        st = torch.empty((T // GROUP, 2 * F), dtype=torch.float32, device=dev)
+    groups = expert_columns(M, _offsets(wh, off, dh.device)) // GROUP
+    q, s, qt, st = _both_forms(stream, dh.device, M, F, groups, rows, tokens)
     fp8q_grouped_gated_backward(dh, gate_up, off, q, s, qt, st, act, mode, stream)
     return q, s, qt, st
 
@@ -1229,7 +1241,7 @@ def grouped_gemm_rowscaled(a_q, a_s, b_q, b_s, off, out_dtype=None, stream=None,
     import torch
     N, K = _rows(wh, a_q, b_q)
     G = _offsets(wh, off, a_q.device)
-    c = torch.empty((G, N, K), dtype=out_dtype or torch.float32, device=a_q.device)
+    (c,) = _new(stream, a_q.device, ((G, N, K), out_dtype or torch.float32))
     f = fp8q_grouped_gemm_rowscaled_precise if precise else fp8q_grouped_gemm_rowscaled
     f(a_q, a_s, b_q, b_s, off, c, stream)
     return c
