@@ -1280,6 +1280,8 @@ def adamw_8bit(params, grads, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_
     [ceil(n/128)]).  Zero codes and scales are the state before the first step.
     The codes are rounded with a dither of the element's place and the step, so
     that a moment which moves by less than a code's step each time does not stay
-    where it is."""
+    where it is.  An element whose gradient is not finite, or so large that its
+    square overflows, is NaN from the next step on at the latest; the others of
+    its group keep their moments."""
     _adamw(params, grads, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, step, lr,
            betas, eps, weight_decay, grad_scale, copies, stream)

@@ -588,7 +588,7 @@ fp8q_status fp8q_grouped_gemm_rowscaled_precise(const uint8_t* a_q, const float*
  *
  * Moments in E4M3 (FP8Q_MOMENTS_E4M3): m holds codes of m and v codes of r = sqrt(v),
  * each 128 consecutive elements of a tensor (the last ones fewer) with one scale,
- * m_s and v_s: fl(amax * fl(1/448)) of their largest magnitude amax, multiplier
+ * m_s and v_s: fl(amax * fl(1/448)) of their largest finite magnitude amax, multiplier
  * fl(448 * fl(1/amax)) (not finite: scale and codes are 0).  m = code * scale, v =
  * fl(r r), r = code * scale go into the formulas above; then x = fl(m * multiplier)
  * and the same of r are rounded with a dither instead of to the nearest, so that a
@@ -599,6 +599,9 @@ fp8q_status fp8q_grouped_gemm_rowscaled_precise(const uint8_t* a_q, const float*
  * of the element's place i in its tensor and the step's number for m, 2^20 - 1 - u
  * for r; a r that is not zero becomes 2^-9 at least.  (The fraction is of FP32's bits:
  * below 2^-6, of |x| + 2^-6 rounded to FP32.)
+ * A m or r that is not finite (of a gradient that is not, or whose square overflows)
+ * becomes the code of NaN, 0x7F, with no part in amax: its own parameter is NaN from the
+ * next step on at the latest, the others of its group are as without it.
  */
 typedef enum {
   FP8Q_MOMENTS_F32 = 0,  /* m, v: float32 [n]                                       */

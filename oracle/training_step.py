@@ -94,9 +94,12 @@ def dither(n, step, second=False, first=0):
 
 def encode_moments(x, step, second=False, first=0):
     """(codes, scales) of float32 x[n] (second: a root, >= 0), bit for bit; x[0] is
-    element `first` of its tensor."""
+    element `first` of its tensor.  What is not finite gets the code of NaN and has no
+    part in its group's scale."""
     x = np.asarray(x, dtype=F32)
     n = x.size
+    finite = np.isfinite(x)
+    x = np.where(finite, x, F32(0))
     amax = np.abs(_grouped(x)).max(axis=1)
     with np.errstate(divide="ignore", over="ignore"):
         mul = F32(448) * (F32(1) / amax)
@@ -113,4 +116,5 @@ def encode_moments(x, step, second=False, first=0):
     if second:
         r = np.where((r == 0) & (a > 0), F32(2.0 ** -9), r)
     codes = e4m3.encode(r.astype(np.float64))   # (exact: r is an E4M3 value)
-    return np.where(np.signbit(y), codes | 0x80, codes).astype(np.uint8), scales.astype(F32)
+    codes = np.where(np.signbit(y), codes | 0x80, codes)
+    return np.where(finite, codes, 0x7F).astype(np.uint8), scales.astype(F32)
