@@ -64,7 +64,7 @@ struct AdamwScalars {
   const float* lr;  // on the device, or NULL
   const int32_t* step;
   const float* grad_scale;
-  double log_b1, log_b2, lr_host, decay;
+  double log_b1, log_b2, lr_host, decay, c1;  // c1: 1 - b1^t
   float b1, one_b1, b2, one_b2, eps;
   float keep, rate, inv_root;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   uint32_t dither;             // t's part of the dither
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_
       inv_root = (float)(1.0 / sqrt(-expm1((double)st * a.log_b2)));
       step_dither = (uint32_t)st * kDitherStep;
     } else {
-      rate = (float)(lr * (double)a.rate);  // a.rate: 1 / (1 - b1^t)
+      rate = (float)(lr / a.c1);
     }
   }
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
@@ -443,8 +443,9 @@ hipError_t launch_adamw(const fp8q_adamw_tensor* tensors, int32_t count, const f
   a.eps = (float)h.eps;
   a.keep = (float)(1.0 - h.lr * h.weight_decay);
   // 1 - beta^t cancels for a beta near 1: from the logarithm, in 64 bits
-  const double c1 = -expm1((double)h.step * a.log_b1), c2 = -expm1((double)h.step * a.log_b2);
-  a.rate = (float)((h.lr_dev ? 1.0 : h.lr) / c1);
+  const double c2 = -expm1((double)h.step * a.log_b2);
+  a.c1 = -expm1((double)h.step * a.log_b1);
+  a.rate = (float)(h.lr / a.c1);
   a.inv_root = (float)(1.0 / sqrt(c2));
   a.dither = (uint32_t)h.step * kDitherStep;
   auto f = e4m3 ? (grad_bf16 ? launches<true, true> : launches<true, false>)
