@@ -802,6 +802,8 @@ def _adamw_args(where, step, lr, betas, eps, weight_decay, grad_scale, dev):
     for n, v in values:
         if not 0 <= v < (1 if n.startswith("beta") else float("inf")):
             raise ValueError(f"{where}: {n} = {v}")
+    if a.eps and not 2.0 ** -126 <= a.eps <= 2.0 ** 125:
+        raise ValueError(f"{where}: eps = {a.eps}, expected 0 or 2^-126 to 2^125")
     if not a.step_dev and a.step < 1:
         raise ValueError(f"{where}: step = {step}, the first is 1")
     return a

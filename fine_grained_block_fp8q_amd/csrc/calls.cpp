@@ -533,7 +533,8 @@ PyObject* adamw(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     // (values out of range: the Python path says which)
     auto bad = [](double x, double end) { return !(x >= 0.0 && x < end); };
     if (!c.ok || bad(a.lr, INFINITY) || bad(a.beta1, 1) || bad(a.beta2, 1) ||
-        bad(a.eps, INFINITY) || bad(a.weight_decay, INFINITY) || (!a.step_dev && a.step < 1))
+        (a.eps != 0.0 && !(a.eps >= 0x1p-126 && a.eps <= 0x1p125)) ||
+        bad(a.weight_decay, INFINITY) || (!a.step_dev && a.step < 1))
       Py_RETURN_NONE;
     const fp8q_status st =
         entries.adamw(list.data(), (int32_t)p.n, &a, type_code(grad->scalar_type()),

@@ -710,6 +710,10 @@ static fp8q_status check_overlap(const fp8q_adamw_tensor* t, int32_t count) {
 
 static bool not_negative(double v) { return v >= 0.0 && isfinite(v); }
 
+// The update's reciprocal takes denominators from 2^-126 to 2^126 (an eps below would be
+// zero to it, and 0/0 of an element without a gradient; root terms stay below 2^92).
+static bool usable_eps(double v) { return v == 0.0 || (v >= 0x1p-126 && v <= 0x1p125); }
+
 fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int32_t count,
                        const fp8q_adamw_args* args, fp8q_out_dtype grad_type,
                        fp8q_moments moments, hipStream_t stream) {
@@ -734,7 +738,7 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int32_t count,
   if (!aligned(args->lr_dev, 4) || !aligned(args->step_dev, 4) || !aligned(args->grad_scale, 4))
     return FP8Q_ERR_ALIGN;
   if (!valid_out(grad_type) || (moments != FP8Q_MOMENTS_F32 && !e4m3)) return FP8Q_ERR_ENUM;
-  if ((!args->lr_dev && !not_negative(args->lr)) || !not_negative(args->eps) ||
+  if ((!args->lr_dev && !not_negative(args->lr)) || !usable_eps(args->eps) ||
       !not_negative(args->weight_decay) || !(args->beta1 >= 0.0 && args->beta1 < 1.0) ||
       !(args->beta2 >= 0.0 && args->beta2 < 1.0) || (!args->step_dev && args->step < 1))
     return FP8Q_ERR_UNSUPPORTED;

@@ -632,8 +632,9 @@ typedef struct {
  *   All data pointers 16-byte aligned, scales and the device scalars 4-byte.
  * A captured call keeps host values: a graph that is replayed step after step takes
  * its step's number (and a changing lr) from the device.
- * FP8Q_ERR_UNSUPPORTED: two tensors' p overlap, n > 2^34, a beta outside [0, 1), lr,
- * eps or weight_decay negative or not finite, or step < 1 (without step_dev).
+ * FP8Q_ERR_UNSUPPORTED: two tensors' p overlap, n > 2^34, a beta outside [0, 1), lr
+ * or weight_decay negative or not finite, eps neither 0 nor in [2^-126, 2^125], or
+ * step < 1 (without step_dev).
  * No other memory of one call may overlap.
  */
 fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int32_t count,
