@@ -35,6 +35,7 @@
 
 #include <type_traits>
 
+#include "activation.hpp"
 #include "fp8q.h"
 #include "launch.hpp"
 #include "fp8q_device.hpp"
@@ -133,8 +134,7 @@ __device__ __forceinline__ v4f unpack_bf16x4(uint32_t lo, uint32_t hi) {
 }
 
 __device__ __forceinline__ v2u pack_bf16x4(const v4f& v) {
-  return v2u{f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16),
-             f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
+  return v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 template <bool E4M3_MOMENTS, bool BF16_GRAD, int CAP>
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_
           m32[i] = m.v[h][j];
           v32[i] = v.v[h][j];
         }
-        if (copy) copy[i] = (uint16_t)f32_to_bf16_bits(p.v[h][j]);
+        if (copy) copy[i] = (uint16_t)pack_bf16x2(p.v[h][j], 0.f);
       }
   }
 }

@@ -20,6 +20,7 @@
 
 #include <type_traits>
 
+#include "activation.hpp"
 #include "fp8q.h"
 #include "launch.hpp"
 #include "quant_rules.hpp"
@@ -106,7 +107,7 @@ __device__ __forceinline__ void store8(void* row, int c, int n, const Row8& r) {
       v4u w;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[j] = f32_to_bf16_bits(r.v[2 * j]) | (f32_to_bf16_bits(r.v[2 * j + 1]) << 16);
+        w[j] = pack_bf16x2(r.v[2 * j], r.v[2 * j + 1]);
       *reinterpret_cast<v4u_any*>(static_cast<uint16_t*>(row) + i) = w;
     } else {
       *reinterpret_cast<v4f_any*>(static_cast<float*>(row) + i) =
@@ -119,7 +120,7 @@ __device__ __forceinline__ void store8(void* row, int c, int n, const Row8& r) {
     for (int j = 0; j < 8; ++j)
       if (i + j < n) {
         if constexpr (BF16)
-          static_cast<uint16_t*>(row)[i + j] = (uint16_t)f32_to_bf16_bits(r.v[j]);
+          static_cast<uint16_t*>(row)[i + j] = (uint16_t)pack_bf16x2(r.v[j], 0.f);
         else
           static_cast<float*>(row)[i + j] = r.v[j];
       }
