@@ -195,6 +195,10 @@ struct NormArgs {
 
 constexpr int kCus = 256;
 
+// Variances (and eps) from here up have lost nothing: a square below FP32's normals is
+// off by 2^-150.
+constexpr float kLeastVar = 0x1p-96f, kMost = 0x1.fffffep127f;
+
 template <int LPR>
 constexpr int kRowThreads = LPR < 256 ? 256 : LPR;
 
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_kernel(const Norm
     for (int k = 0; k < 8; ++k) sum[0] += v[j].v[k];
   }
   row_sum<LPR, 1>(sum, red[0]);
-  const float mean = sum[0] / (float)N;
+  float mean = sum[0] / (float)N;
   float sq[1] = {0.f};
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -241,10 +245,39 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_kernel(const Norm
       sq[0] = __builtin_fmaf(d, d, sq[0]);
     }
   row_sum<LPR, 1>(sq, red[1]);
-  const float rstd = 1.f / __builtin_sqrtf(sq[0] / (float)N + a.eps);
+  float var = sq[0] / (float)N + a.eps, scale = 1.f;
+  if (!(var >= kLeastVar && var <= kMost)) {
+    // Rare, and the same for all lanes of a row: sums that overflow or squares that
+    // underflow.  The row again, large values times 2^-100 or small deviations times
+    // 2^100 (the largest sum of squares is then 2^70, the least square 2^-98).
+    const bool small = var < kLeastVar;
+    const float before = small ? 1.f : 0x1p-100f, after = small ? 0x1p100f : 1.f;
+    sum[0] = sq[0] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      v[j] = load8<X_BF16, WHOLE>(x, l + LPR * j, N);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[0] += v[j].v[k] *= before;
+    }
+    row_sum<LPR, 1>(sum, red[0]);
+    const float m = sum[0] / (float)N;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = 8 * (l + LPR * j) + k < N ? (v[j].v[k] - m) * after : 0.f;
+        v[j].v[k] = d;
+        sq[0] = __builtin_fmaf(d, d, sq[0]);
+      }
+    row_sum<LPR, 1>(sq, red[1]);
+    scale = sq[0] == 0.f ? 1.f : before * after;  // (of a constant row eps alone is left)
+    mean = small ? m : m * 0x1p100f;
+    var = sq[0] / (float)N + a.eps * scale * scale;
+  }
+  const float rstd = 1.f / __builtin_sqrtf(var);  // of the deviations in v
   if (l == 0) {
     a.mean[row] = mean;
-    a.rstd[row] = rstd;
+    a.rstd[row] = rstd * scale;
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {

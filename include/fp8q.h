@@ -496,6 +496,9 @@ fp8q_status fp8q_gated_backward(const void* dh, const void* gate_up, int64_t M, 
  *   |mean - mean_exact| <= D,  rstd within 23 u + (D rstd)^2 / 2 relative,
  *   |z - z_exact| <= rstd D + (25 u + (D rstd)^2 / 2) |z|,  and y within
  *   |weight| times that + 2 u |z weight| + u |y| (and half a BF16 ulp).
+ * This holds for every eps and every row up to |x| = 2^126 of which 1 / sqrt(var + eps)
+ * is a normal FP32 number (rows whose squares FP32 cannot hold are summed scaled by a
+ * power of two).  With eps == 0 a constant row has rstd = infinity and z = NaN.
  */
 fp8q_status fp8q_layer_norm(const void* x, fp8q_out_dtype x_type, const float* weight,
                             const float* bias, int64_t M, int64_t N, float eps, void* y,
