@@ -368,9 +368,13 @@ __global__ __launch_bounds__(kRowThreads<LPR>) void layer_norm_backward_kernel(c
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const Row8 w = load8<false, WHOLE>(a.weight, l + LPR * j, N);
+      // (past the row z is 0 as well: a mean times rstd that overflows would make its
+      // product with dy's 0 a NaN)
+      const float m = !WHOLE || 8 * (l + LPR * j) < N ? mean : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float zz = (z[j].v[k] - mean) * rstd;  // (past the row: times a 0 of dy)
+        const float d = WHOLE || 8 * (l + LPR * j) + k < N ? z[j].v[k] - m : 0.f;
+        const float zz = d * rstd;
         z[j].v[k] = zz;
         dw[j][k] = __builtin_fmaf(g[j].v[k], zz, dw[j][k]);
         db[j][k] += g[j].v[k];
