@@ -453,7 +453,9 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t* a_q, const float* a_s, c
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
     return hipGetLastError();
   const int64_t large = (N + 255) / 256 * ((K + 255) / 256) * G;
-  if (large >= kLargeTiles * cus && !precise)  // (widened to FP16, its fragments would spill)
+  // (Widened to FP16, its fragments would spill.  A resource describes at most 2^32 - 1
+  // bytes: 256 rows of 2^24 are one more.)
+  if (large >= kLargeTiles * cus && !precise && WgLarge::TN * T <= 0xFFFFFFFFll)
     return launch<WgLarge, false>(a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, cus, stream);
   return (precise ? launch<WgSmall, true> : launch<WgSmall, false>)(
       a_q, a_s, b_q, b_s, T, off, G, N, K, c, out_bf16, cus, stream);
