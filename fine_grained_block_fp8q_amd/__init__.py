@@ -169,10 +169,19 @@ class _Bound(Exception):
 _capture = threading.local()
 
 
-def _invoke(cfunc, args, where):
+def _invoke(cfunc, args, where, updated=()):
+    """`updated`: tensors that the call changes in place, of which autograd is to hear."""
     if getattr(_capture, "on", False):
-        raise _Bound((cfunc, args, where))
+        raise _Bound((cfunc, args, where, updated))
     _check(cfunc(*args), where)
+    _bumped(updated)
+
+
+def _bumped(tensors):
+    """Tells autograd that these were written."""
+    if tensors:
+        import torch
+        torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
 
 
 def bind(fn, *args, **kwargs):
@@ -187,7 +196,7 @@ def bind(fn, *args, **kwargs):
     try:
         fn(*args, **kwargs)
     except _Bound as b:
-        cfunc, cargs, where = b.call
+        cfunc, cargs, where, updated = b.call
     else:
         raise TypeError(f"{getattr(fn, '__name__', fn)} is not an entry-point wrapper")
     finally:
@@ -201,6 +210,7 @@ def bind(fn, *args, **kwargs):
         st = cfunc(*cargs)
         if st != OK:
             raise Fp8qError(st, where)
+        _bumped(updated)
     run.args = keep
     return run
 
@@ -809,14 +819,6 @@ def _adamw_args(where, step, lr, betas, eps, weight_decay, grad_scale, dev):
     return a
 
 
-def _bumped(tensors):
-    """Tells autograd that these were written."""
-    import torch
-    for t in tensors:
-        if not t.is_inference():
-            torch.autograd.graph.increment_version(t)
-
-
 def _adamw_call(where, params, grads, m, m_s, v, v_s, step, lr, betas, eps, weight_decay,
                 grad_scale, copies, stream):
     import torch
@@ -854,10 +856,8 @@ def _adamw_call(where, params, grads, m, m_s, v, v_s, step, lr, betas, eps, weig
             a.copy = copies[i].data_ptr()
     args = _adamw_args(where, step, lr, betas, eps, weight_decay, grad_scale, dev)
     _invoke(lib.fp8q_adamw, (array, n, args, grad_type, MOMENTS_E4M3 if eight else MOMENTS_F32,
-                             _stream(stream, dev)), where)
-    for l in (params, m, v, m_s, v_s, copies):
-        if l is not None:
-            _bumped(l)
+                             _stream(stream, dev)), where,
+            [t for l in (params, m, v, m_s, v_s, copies) if l is not None for t in l])
 
 
 def fp8q_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, betas=(0.9, 0.95), eps=1e-8,
