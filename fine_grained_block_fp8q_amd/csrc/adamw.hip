@@ -6,8 +6,8 @@
 // masters in FP32, moments in FP32 or in 8 bits.  Bound by memory: a master is
 // read and written (8 bytes), the gradient read (2 or 4), the moments read and
 // written (16, or 4 and the scales), the BF16 copy written (2).  44M parameters,
-// moments in FP32, BF16 gradients and copy: 197 us (6.2 TB/s); 340M, moments in 8
-// bits: 935 us (5.9 TB/s), near which the vector ALU's work comes too.
+// moments in FP32, BF16 gradients and copy: 195 to 199 us (6.2 TB/s); 340M, moments in
+// 8 bits: 921 to 932 us (5.9 TB/s), near which the vector ALU's work comes too.
 //
 // Moments in 8 bits: E4M3 codes of m' and of sqrt(v') (the root has half the
 // exponent range of v', so 128 elements of one scale reach 2^35 down from the
@@ -172,8 +172,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwLaunch<E4M3_
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
 
   // The lane's two fours lie 64 apart, so that 16 lanes' accesses of FP32 are 256
-  // consecutive bytes (eight consecutive elements a lane: 1010 us for 340M parameters
-  // with moments in 8 bits, so 935).
+  // consecutive bytes (340M parameters with moments in 8 bits: 935 us, with eight
+  // consecutive elements a lane 1010).
   const uint32_t l16 = lane & 15, group = (threadIdx.x >> 4) * kGroup;
   if ((int)group >= rest) return;  // (whole DPP rows)
   constexpr uint32_t kApart = 64;

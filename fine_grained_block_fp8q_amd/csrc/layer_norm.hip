@@ -9,14 +9,19 @@
 // the registers, and y leaves as E4M3 codes (128 consecutive elements are one DPP
 // row of 16 lanes, so a group's maximum costs four instructions), as BF16 or
 // FP32, or both: bound by memory.  The codes are those of y in FP32, not of its
-// BF16 rounding.  4096 rows of 7168, FP32 in, codes and BF16 out: 41.2 us (5.0 TB/s,
-// a copy's rate).
+// BF16 rounding.  4096 rows of 7168, FP32 in, codes and BF16 out: 41 us over two sets of
+// inputs in turn (5.0 TB/s, a copy's rate), 45 over more of them.
+//
+// Rows whose squares or sums leave FP32's range are read and summed again, scaled by a
+// power of two; the others pay a comparison for it (under 1%).
 //
 // Backward: each workgroup walks rows and keeps its columns' sums of dy z and dy
 // in registers; they go to a workspace, one row of it a workgroup, which a second
 // kernel adds up in a fixed order (no atomics: the same bits every time).  4096 rows of
-// 7168, x and dx in FP32, dy in BF16: 68 us (4.3 TB/s); what the workgroups leave, 15 MB
-// that are written and read, takes 7 of them.
+// 7168, x and dx in FP32, dy in BF16: 68 to 71 us (4.2 TB/s); what the workgroups leave,
+// 15 MB that are written and read, takes 7 of them.  Five kernels for widths that are no
+// multiple of 8 keep 7 to 13 registers in scratch memory: FP32 x and dy of 4097 to 8192
+// columns, and all types above 8192.
 
 #include <type_traits>
 
